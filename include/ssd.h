@@ -561,6 +561,146 @@ int ssd_linear_fwd_ev(const void *x, int x_dtype, const void *W, void *z,
 int ssd_mimo_fwd(const void *y, int y_dtype, const void *W, void *z,
                  int z_dtype, int Bsz, int T, int H, int P, void *stream);
 
+/*
+ * Residual update and pre-norm of a block (block page: RMSNorm, pre-norm, eps
+ * 1e-5), row by row:
+ *   r   = residual + scale o x
+ *   out = r / sqrt(mean(r^2) + eps) o w        (r in float32, before rounding)
+ *   x            (M, D)  x_dtype (SSD_F32 or SSD_BF16): the block's output
+ *   scale        (D)     float32 residual scale per channel, or NULL (1)
+ *   residual     (M, D)  res_dtype, or NULL (zero)
+ *   w            (D)     float32
+ *   residual_out (M, D)  res_dtype, r rounded once, or NULL (not written);
+ *                        may be `residual` itself (updated in place)
+ *   out          (M, D)  out_dtype, rounded once
+ * M >= 0 rows of D channels, 1 <= D <= 16384, any alignment of the element
+ * size.  Sums are float32: |r| stays below about 1e18 (its squares do not
+ * overflow).  Apart from residual_out, outputs must not overlap inputs (such a
+ * call is rejected).  Errors: SSD_EINVAL, SSD_EUNSUPPORTED (dtype, D), SSD_EHIP.
+ */
+int ssd_add_norm_fwd(const void *x, const float *scale, const void *residual,
+                     const float *w, float eps, void *residual_out, void *out,
+                     int M, int D, int x_dtype, int res_dtype, int out_dtype,
+                     void *stream);
+
+/*
+ * Backward of ssd_add_norm_fwd: the gradient of <dout, out> + <dres,
+ * residual_out>, taken at the given r.
+ *   dout      (M, D)  out_dtype
+ *   dres      (M, D)  res_dtype, gradient of residual_out, or NULL (zero)
+ *   r         (M, D)  res_dtype, the forward's residual_out
+ *   x         (M, D)  x_dtype, the forward's x; read only for dscale (may be
+ *                     NULL without it)
+ *   dresidual (M, D)  res_dtype, or NULL (not written)
+ *   dx        (M, D)  x_dtype, or NULL
+ *   dw        (D)     float32, summed over the rows
+ *   dscale    (D)     float32, summed over the rows, or NULL
+ *   workspace ssd_add_norm_bwd_workspace_size(M, D) bytes, 256-byte aligned
+ * Sums over rows are made in a fixed order (no atomics): the same call gives
+ * the same bits.  Outputs are overwritten and must not overlap anything.
+ */
+size_t ssd_add_norm_bwd_workspace_size(int M, int D);
+int ssd_add_norm_bwd(const void *dout, const void *dres, const void *r,
+                     const void *x, const float *scale, const float *w,
+                     float eps, void *dresidual, void *dx, float *dw,
+                     float *dscale, int M, int D, int x_dtype, int res_dtype,
+                     int out_dtype, void *workspace, size_t workspace_bytes,
+                     void *stream);
+
+/*
+ * Gated norm between the scan and out_proj of a Mamba-2 layer, per row and per
+ * group of L = D / groups consecutive channels, s = z / (1 + exp(-z)):
+ *   norm_before_gate 0:  u = y o s, out = u / sqrt(mean_group(u^2) + eps) o w
+ *   norm_before_gate 1:  out = y / sqrt(mean_group(y^2) + eps) o w o s
+ *   y    (M, D)   y_dtype: the scan's (Bsz, T, H, P) or the step's (Bsz, H, P)
+ *   z    M rows of D elements, ldz elements apart (ldz >= D; the in_proj rows
+ *        in place), z_dtype
+ *   w    (D)      float32
+ *   out  (M, D)   out_dtype, rounded once
+ * 1 <= L <= 16384, any alignment of the element size.  Limits, overlap and
+ * errors as in ssd_add_norm_fwd.
+ */
+int ssd_gated_norm_fwd(const void *y, const void *z, long long ldz,
+                       const float *w, float eps, int norm_before_gate,
+                       void *out, int M, int D, int groups, int y_dtype,
+                       int z_dtype, int out_dtype, void *stream);
+
+/*
+ * Backward of ssd_gated_norm_fwd for the gradient dout (M, D) out_dtype:
+ *   dy   (M, D)   y_dtype
+ *   dz   M rows of D elements, lddz apart, z_dtype (the in_proj gradient's
+ *        rows in place; columns past D are left as they are)
+ *   dw   (D)      float32, summed over the rows
+ *   workspace     ssd_gated_norm_bwd_workspace_size(M, D, groups) bytes,
+ *                 256-byte aligned
+ */
+size_t ssd_gated_norm_bwd_workspace_size(int M, int D, int groups);
+int ssd_gated_norm_bwd(const void *dout, const void *y, const void *z,
+                       long long ldz, const float *w, float eps,
+                       int norm_before_gate, void *dy, void *dz, long long lddz,
+                       float *dw, int M, int D, int groups, int y_dtype,
+                       int z_dtype, int out_dtype, void *workspace,
+                       size_t workspace_bytes, void *stream);
+
+/*
+ * Backward of ssd_conv1d_fwd: the gradient of <dx, x> + <dB, B> + <dC, C> +
+ * <dstate_out, state_out>.
+ *   xbc, ld, w, bias, state_in, act, HP, GN, K, dtype as given to the forward
+ *   dx         (Bsz, T, HP)  dtype      (ssd_chunk_bwd's dx)
+ *   dB, dC     (Bsz, T, GN)  float32    (ssd_chunk_bwd's dB, dC)
+ *   dstate_out (Bsz, 3, Ch)  float32, or NULL (zero)
+ *   dxbc       (Bsz, T, lddx) rows of dtype: columns 0..Ch-1 written, the
+ *              others left as they are (the in_proj gradient's rows in place)
+ *   dw         (Ch, 4) float32, dbias (Ch) float32: summed over batch and
+ *              tokens, written even when bias is NULL
+ *   dstate_in  (Bsz, 3, Ch) float32, or NULL (not written)
+ *   workspace  ssd_conv1d_bwd_workspace_size(...) bytes, 256-byte aligned
+ * HP, GN, ld and lddx multiples of 8 (bf16) or 4 (fp32), pointers 16-byte
+ * aligned, T <= 2^30, Ch <= 2^24.  T = 0: dstate_in is dstate_out, the sums
+ * are zero.  Sums in a fixed order (no atomics).  Outputs must not overlap
+ * anything (such a call is rejected).
+ */
+size_t ssd_conv1d_bwd_workspace_size(int Bsz, int T, int HP, int GN);
+int ssd_conv1d_bwd(const void *xbc, long long ld, const float *w,
+                   const float *bias, const float *state_in, int act,
+                   const void *dx, const float *dB, const float *dC,
+                   const float *dstate_out, void *dxbc, long long lddx,
+                   float *dw, float *dbias, float *dstate_in, int Bsz, int T,
+                   int HP, int GN, int K, int dtype, void *workspace,
+                   size_t workspace_bytes, void *stream);
+
+/*
+ * One token per sequence through the convolution and the recurrence in one
+ * launch (ssd_conv1d_step, then ssd_step_decode on its outputs), on a pool of
+ * states, for serving loops whose batch changes from step to step.
+ *   conv_state (nslots, 3, Ch)    float32, the layout of ssd_conv1d_fwd's
+ *                                 state_out; Ch = H P + 2 G N
+ *   h          (nslots, H, P, N)  float32
+ *   arrivals   (nslots, G)        int32, zero when the pool is made and owned
+ *                                 by the library from then on (each call
+ *                                 leaves it zero).  May be NULL when H == G.
+ *   slots      (Bsz) int32, DEVICE memory: row b's slot, or NULL (row b has
+ *              slot b, Bsz <= nslots).  A row whose slot is outside [0,
+ *              nslots) is a padding row, and so is one whose slot an earlier
+ *              row has: its y is zero and no state is touched.
+ *   xbc        Bsz rows of Ch elements of `dtype`, ldx apart; dt: Bsz rows of
+ *              H elements of `dtype`, lddt apart (both in place in the in_proj
+ *              rows; any alignment of the element size)
+ *   w (Ch, 4), bias (Ch) or NULL, act  as in ssd_conv1d_step
+ *   A, D, dt_bias, dt_min, dt_max      as in ssd_step_decode
+ *   y          (Bsz, H, P) y_dtype
+ * Both states of every named slot are updated in place.  P <= 1024, N in {16,
+ * 32, 64, 128, 256}, K = 4; h and w 16-byte aligned.  Calls that share no slot
+ * may run at the same time; calls that share one must be ordered.  No
+ * workspace.  Arrays that are written must not overlap any other.
+ */
+int ssd_mixer_step(float *conv_state, float *h, int *arrivals, const int *slots,
+                   int nslots, const void *xbc, long long ldx, const void *dt,
+                   long long lddt, const float *w, const float *bias, int act,
+                   const float *A, const float *D, const float *dt_bias,
+                   float dt_min, float dt_max, void *y, int y_dtype, int Bsz,
+                   int H, int P, int G, int N, int K, int dtype, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

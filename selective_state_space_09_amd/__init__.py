@@ -111,6 +111,26 @@ def lib():
     L.ssd_conv1d_step.argtypes = [P, P, LL, P, P, I, P, P, P, I, I, I, I, P]
     L.ssd_conv1d_step_ev.restype = I
     L.ssd_conv1d_step_ev.argtypes = L.ssd_conv1d_step.argtypes + [P]
+    L.ssd_add_norm_fwd.restype = I
+    L.ssd_add_norm_fwd.argtypes = [P, P, P, P, F, P, P, I, I, I, I, I, P]
+    L.ssd_add_norm_bwd_workspace_size.restype = S
+    L.ssd_add_norm_bwd_workspace_size.argtypes = [I, I]
+    L.ssd_add_norm_bwd.restype = I
+    L.ssd_add_norm_bwd.argtypes = [P, P, P, P, P, P, F, P, P, P, P, I, I, I, I, I, P, S, P]
+    L.ssd_gated_norm_fwd.restype = I
+    L.ssd_gated_norm_fwd.argtypes = [P, P, LL, P, F, I, P, I, I, I, I, I, I, P]
+    L.ssd_gated_norm_bwd_workspace_size.restype = S
+    L.ssd_gated_norm_bwd_workspace_size.argtypes = [I, I, I]
+    L.ssd_gated_norm_bwd.restype = I
+    L.ssd_gated_norm_bwd.argtypes = [P, P, P, LL, P, F, I, P, P, LL, P, I, I, I, I, I, I, P, S, P]
+    L.ssd_conv1d_bwd_workspace_size.restype = S
+    L.ssd_conv1d_bwd_workspace_size.argtypes = [I, I, I, I]
+    L.ssd_conv1d_bwd.restype = I
+    L.ssd_conv1d_bwd.argtypes = [P, LL, P, P, P, I, P, P, P, P, P, LL, P, P, P, I, I, I, I, I, I,
+                                 P, S, P]
+    L.ssd_mixer_step.restype = I
+    L.ssd_mixer_step.argtypes = [P, P, P, P, I, P, LL, P, LL, P, P, I, P, P, P, F, F, P, I,
+                                 I, I, I, I, I, I, I, P]
     _lib = L
     return L
 
@@ -779,3 +799,322 @@ def ssd_mimo_fwd(y, W, z=None, out_dtype=torch.bfloat16, stream=None):
     _dev(z, "z")
     _check(lib().ssd_mimo_fwd(_ptr(y), yd, _ptr(W), _ptr(z), zd, Bsz, T, H, P, _stream(stream)))
     return z
+
+
+class _SameDevice:
+    """The scope of a call on the current device and stream: nothing to do."""
+
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return False
+
+
+_SAME_DEVICE = _SameDevice()
+
+
+def _scope(t, stream):
+    """Context that makes t's device, and the call's stream on it, current, so
+    that what a call allocates belongs to the stream it runs on and the launch
+    goes to t's device."""
+    if stream is not None:
+        if stream.device != t.device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
+        return torch.cuda.stream(stream)
+    if t.device.index == torch.cuda.current_device():
+        return _SAME_DEVICE
+    return torch.cuda.device(t.device)
+
+
+def _tensors(ref, *specs):
+    """Pointers of the arguments (tensor or None, name, shape, dtype): every
+    shape and type is checked before any device, each must be contiguous on
+    ref's GPU."""
+    for t, name, shape, dtype in specs:
+        if t is None:
+            continue
+        if t.shape != shape:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    out = []
+    dev = ref.device
+    for t, name, shape, dtype in specs:
+        if t is None:
+            out.append(None)
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a GPU tensor")
+        if t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        out.append(t.data_ptr())
+    return out
+
+
+def _rows_like(t, name, shape, dtype, ref):
+    """Shape, type and device of a strided argument (see _lead)."""
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != ref.device:
+        raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
+
+
+def _lead(t, name):
+    """Rows of the last axis of a tensor whose leading axes collapse into one
+    evenly spaced axis (contiguous, or a column slice of such rows): their
+    stride in elements."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a GPU tensor")
+    if t.numel() == 0 or t.is_contiguous():
+        return max(t.shape[-1], 1)
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have a contiguous last dim")
+    ld = span = None
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if ld is None:
+            ld = stride
+        elif stride != span:
+            raise ValueError(f"{name}: its rows must be evenly spaced")
+        span = stride * size
+    if ld is None:
+        return t.shape[-1]
+    if ld < t.shape[-1]:
+        raise ValueError(f"{name}: rows {ld} apart overlap, they have {t.shape[-1]} elements")
+    return ld
+
+
+def _scratch(nbytes, ref, workspace):
+    if workspace is None:
+        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=ref.device)
+    _tensors(ref, (workspace, "workspace", workspace.shape, torch.uint8))
+    return workspace
+
+
+def ssd_add_norm_bwd_workspace_size(M, D):
+    return int(lib().ssd_add_norm_bwd_workspace_size(M, D))
+
+
+def ssd_gated_norm_bwd_workspace_size(M, D, groups=1):
+    return int(lib().ssd_gated_norm_bwd_workspace_size(M, D, groups))
+
+
+def ssd_conv1d_bwd_workspace_size(Bsz, T, HP, GN):
+    return int(lib().ssd_conv1d_bwd_workspace_size(Bsz, T, HP, GN))
+
+
+def _rows_of(x, name):
+    if x.dim() < 1 or x.shape[-1] < 1:
+        raise ValueError(f"{name} must have rows of at least one channel, got shape {tuple(x.shape)}")
+    return x.shape[-1], x.numel() // x.shape[-1]
+
+
+def ssd_add_norm_fwd(x, w, residual=None, scale=None, eps=1e-5, out=None, out_dtype=None,
+                     residual_out=None, res_dtype=None, stream=None):
+    """Residual update and pre-norm of a block: r = residual + scale * x, out =
+    r / sqrt(mean(r^2) + eps) * w over the last axis.  x, residual (..., D)
+    contiguous, float32 or bfloat16 each; w, scale (D) float32; residual and
+    scale may be None (0, 1).  out has out_dtype (default x's), r the type of
+    residual (default float32, or res_dtype); residual_out may be residual
+    itself.  Returns (out, r)."""
+    D, M = _rows_of(x, "x")
+    shape = x.shape
+    xd = _dcode(x.dtype, "x")
+    if residual is not None:
+        if res_dtype not in (None, residual.dtype):
+            raise TypeError(f"residual is {residual.dtype}, res_dtype {res_dtype}")
+        res_dtype = residual.dtype
+    elif res_dtype is None:
+        res_dtype = torch.float32 if residual_out is None else residual_out.dtype
+    if out_dtype is None:
+        out_dtype = x.dtype if out is None else out.dtype
+    rd, od = _dcode(res_dtype, "residual"), _dcode(out_dtype, "out")
+    f32 = torch.float32
+    px, ps, pr, pw, pro, po = _tensors(
+        x, (x, "x", shape, x.dtype), (scale, "scale", (D,), f32),
+        (residual, "residual", shape, res_dtype), (w, "w", (D,), f32),
+        (residual_out, "residual_out", shape, res_dtype), (out, "out", shape, out_dtype))
+    with _scope(x, stream):
+        if out is None:
+            out = torch.empty(shape, dtype=out_dtype, device=x.device)
+            po = out.data_ptr()
+        if residual_out is None:
+            residual_out = torch.empty(shape, dtype=res_dtype, device=x.device)
+            pro = residual_out.data_ptr()
+        _check(lib().ssd_add_norm_fwd(px, ps, pr, pw, eps, pro, po, M, D, xd, rd, od,
+                                      _stream(stream)))
+    return out, residual_out
+
+
+def ssd_add_norm_bwd(dout, r, w, dres=None, scale=None, x=None, eps=1e-5, x_dtype=None,
+                     workspace=None, stream=None):
+    """Gradient of sum(dout * out) + sum(dres * r) of ssd_add_norm_fwd at its r.
+    dout (..., D) in out's type, r and dres (..., D) in the residual's, x (the
+    forward's, needed for dscale only).  Returns a dict: dresidual (r's type),
+    dx (x_dtype; default x's type, or dout's), dw (D) float32 and dscale (D)
+    float32 (None unless x is given)."""
+    D, M = _rows_of(r, "r")
+    shape = r.shape
+    if x_dtype is None:
+        x_dtype = dout.dtype if x is None else x.dtype
+    xd, rd, od = _dcode(x_dtype, "x"), _dcode(r.dtype, "r"), _dcode(dout.dtype, "dout")
+    f32 = torch.float32
+    pr, pd, pe, px, pw, ps = _tensors(
+        r, (r, "r", shape, r.dtype), (dout, "dout", shape, dout.dtype),
+        (dres, "dres", shape, r.dtype), (x, "x", shape, x_dtype), (w, "w", (D,), f32),
+        (scale, "scale", (D,), f32))
+    with _scope(r, stream):
+        dresidual = torch.empty(shape, dtype=r.dtype, device=r.device)
+        dx = torch.empty(shape, dtype=x_dtype, device=r.device)
+        dw = torch.empty(D, dtype=f32, device=r.device)
+        ds = None if x is None else torch.empty(D, dtype=f32, device=r.device)
+        ws = _scratch(ssd_add_norm_bwd_workspace_size(M, D), r, workspace)
+        _check(lib().ssd_add_norm_bwd(pd, pe, pr, px, ps, pw, eps, dresidual.data_ptr(),
+                                      dx.data_ptr(), dw.data_ptr(),
+                                      None if ds is None else ds.data_ptr(), M, D, xd, rd, od,
+                                      ws.data_ptr(), ws.numel(), _stream(stream)))
+    return dict(dresidual=dresidual, dx=dx, dw=dw, dscale=ds)
+
+
+def ssd_gated_norm_fwd(y, z, w, groups=1, eps=1e-5, norm_before_gate=False, out=None,
+                       out_dtype=None, stream=None):
+    """Gated norm between the scan and out_proj over the last axis, per group of
+    D / groups channels: rms(y * silu(z)) * w, or with norm_before_gate
+    rms(y) * w * silu(z).  y (..., D) contiguous; z of y's shape, contiguous or
+    a column slice of evenly spaced rows (the in_proj rows); float32 or bfloat16
+    each; w (D) float32.  Returns out (..., D) in out_dtype (default z's)."""
+    D, M = _rows_of(y, "y")
+    shape = y.shape
+    if out_dtype is None:
+        out_dtype = z.dtype if out is None else out.dtype
+    yd, zd, od = _dcode(y.dtype, "y"), _dcode(z.dtype, "z"), _dcode(out_dtype, "out")
+    _rows_like(z, "z", shape, z.dtype, y)
+    py, pw, po = _tensors(y, (y, "y", shape, y.dtype), (w, "w", (D,), torch.float32),
+                          (out, "out", shape, out_dtype))
+    ldz = _lead(z, "z")
+    with _scope(y, stream):
+        if out is None:
+            out = torch.empty(shape, dtype=out_dtype, device=y.device)
+            po = out.data_ptr()
+        _check(lib().ssd_gated_norm_fwd(py, z.data_ptr(), ldz, pw, eps, int(bool(norm_before_gate)),
+                                        po, M, D, groups, yd, zd, od, _stream(stream)))
+    return out
+
+
+def ssd_gated_norm_bwd(dout, y, z, w, groups=1, eps=1e-5, norm_before_gate=False, dz=None,
+                       workspace=None, stream=None):
+    """Gradient of sum(dout * out) of ssd_gated_norm_fwd.  dz may be given as a
+    column slice of evenly spaced rows (the in_proj gradient's; other columns
+    are left as they are).  Returns a dict: dy (y's type), dz (z's type), dw (D)
+    float32."""
+    D, M = _rows_of(y, "y")
+    shape = y.shape
+    yd, zd, od = _dcode(y.dtype, "y"), _dcode(z.dtype, "z"), _dcode(dout.dtype, "dout")
+    _rows_like(z, "z", shape, z.dtype, y)
+    if dz is not None:
+        _rows_like(dz, "dz", shape, z.dtype, y)
+    py, pd, pw = _tensors(y, (y, "y", shape, y.dtype), (dout, "dout", shape, dout.dtype),
+                          (w, "w", (D,), torch.float32))
+    ldz = _lead(z, "z")
+    with _scope(y, stream):
+        if dz is None:
+            dz = torch.empty(shape, dtype=z.dtype, device=y.device)
+        dy = torch.empty(shape, dtype=y.dtype, device=y.device)
+        dw = torch.empty(D, dtype=torch.float32, device=y.device)
+        ws = _scratch(ssd_gated_norm_bwd_workspace_size(M, D, groups), y, workspace)
+        _check(lib().ssd_gated_norm_bwd(pd, py, z.data_ptr(), ldz, pw, eps,
+                                        int(bool(norm_before_gate)), dy.data_ptr(), dz.data_ptr(),
+                                        _lead(dz, "dz"), dw.data_ptr(), M, D, groups, yd, zd, od,
+                                        ws.data_ptr(), ws.numel(), _stream(stream)))
+    return dict(dy=dy, dz=dz, dw=dw)
+
+
+def ssd_conv1d_bwd(xbc, w, dx, dB, dC, bias=None, state_in=None, dstate_out=None, act=1, dxbc=None,
+                   want_dstate_in=True, workspace=None, stream=None):
+    """Gradient of sum(dx * x) + sum(dB * B) + sum(dC * C) + sum(dstate_out *
+    state_out) of ssd_conv1d_fwd.  xbc, w, bias, state_in, act as given to the
+    forward; dx (Bsz,T,HP) in xbc's type, dB and dC (Bsz,T,GN) float32 (what
+    ssd_chunk_bwd returns, flattened), dstate_out (Bsz,3,Ch) float32.  dxbc may
+    be given as a column slice of evenly spaced rows (other columns are left as
+    they are).  Returns a dict: dxbc (xbc's type), dw (Ch,4), dbias (Ch) and
+    dstate_in (Bsz,3,Ch; None unless want_dstate_in), float32."""
+    _ndim(xbc, "xbc", 3)
+    _ndim(dx, "dx", 3)
+    _ndim(dB, "dB", 3)
+    _ndim(w, "w", 2)
+    Bsz, T, Ch = xbc.shape
+    HP, GN, K = dx.shape[2], dB.shape[2], w.shape[1]
+    if Ch != HP + 2 * GN:
+        raise ValueError(f"xbc has {Ch} channels, HP + 2*GN = {HP + 2 * GN}")
+    code = _dcode(xbc.dtype, "xbc")
+    f32 = torch.float32
+    if dxbc is not None:
+        _rows_like(dxbc, "dxbc", (Bsz, T, Ch), xbc.dtype, xbc)
+    pw, px, pb, pc, pi, ps, pe = _tensors(
+        xbc, (w, "w", (Ch, K), f32), (dx, "dx", (Bsz, T, HP), xbc.dtype),
+        (dB, "dB", (Bsz, T, GN), f32), (dC, "dC", (Bsz, T, GN), f32), (bias, "bias", (Ch,), f32),
+        (state_in, "state_in", (Bsz, K - 1, Ch), f32),
+        (dstate_out, "dstate_out", (Bsz, K - 1, Ch), f32))
+    ld = _lead(xbc, "xbc")
+    dev = xbc.device
+    with _scope(xbc, stream):
+        if dxbc is None:
+            dxbc = torch.empty((Bsz, T, Ch), dtype=xbc.dtype, device=dev)
+        dw = torch.empty((Ch, K), dtype=f32, device=dev)
+        dbias = torch.empty(Ch, dtype=f32, device=dev)
+        dstate = torch.empty((Bsz, K - 1, Ch), dtype=f32, device=dev) if want_dstate_in else None
+        ws = _scratch(ssd_conv1d_bwd_workspace_size(Bsz, T, HP, GN), xbc, workspace)
+        _check(lib().ssd_conv1d_bwd(xbc.data_ptr(), ld, pw, pi, ps, int(act), px, pb, pc, pe,
+                                    dxbc.data_ptr(), _lead(dxbc, "dxbc"), dw.data_ptr(),
+                                    dbias.data_ptr(), None if dstate is None else dstate.data_ptr(),
+                                    Bsz, T, HP, GN, K, code, ws.data_ptr(), ws.numel(),
+                                    _stream(stream)))
+    return dict(dxbc=dxbc, dw=dw, dbias=dbias, dstate_in=dstate)
+
+
+def ssd_mixer_step(conv_state, h, arrivals, xbc, dt, w, A, bias=None, D=None, dt_bias=None,
+                   dt_min=0.0, dt_max=math.inf, slots=None, act=1, y=None, y_dtype=torch.float32,
+                   stream=None):
+    """One token per sequence through the convolution and the recurrence, on a
+    pool of states updated in place: conv_state (nslots,3,Ch) and h
+    (nslots,H,P,N) float32, arrivals (nslots,G) int32 (zeros when the pool is
+    made, then the library's; None allowed when H == G).  slots (Bsz) int32 on
+    the GPU maps rows to slots (None: row b has slot b); a row whose slot is
+    outside the pool, or taken by an earlier row, is padding: its y is zero.
+    xbc (Bsz,Ch) and dt (Bsz,H) float32 or bfloat16, contiguous or column slices
+    of the in_proj rows.  Returns y (Bsz,H,P) in y_dtype."""
+    _ndim(h, "h", 4)
+    _ndim(xbc, "xbc", 2)
+    _ndim(w, "w", 2)
+    nslots, H, P, N = h.shape
+    Bsz, Ch = xbc.shape
+    if Ch <= H * P or (Ch - H * P) % (2 * N):
+        raise ValueError(f"xbc has {Ch} channels, not H*P + 2*G*N with H={H} P={P} N={N}")
+    G, K = (Ch - H * P) // (2 * N), w.shape[1]
+    code = _dcode(xbc.dtype, "xbc")
+    f32 = torch.float32
+    if y is not None:
+        y_dtype = y.dtype
+    yd = _dcode(y_dtype, "y")
+    _rows_like(xbc, "xbc", (Bsz, Ch), xbc.dtype, h)
+    _rows_like(dt, "dt", (Bsz, H), xbc.dtype, h)
+    ph, ps, pa, pm, pw, pA, pi, pD, pt, py = _tensors(
+        h, (h, "h", h.shape, f32), (conv_state, "conv_state", (nslots, K - 1, Ch), f32),
+        (arrivals, "arrivals", (nslots, G), torch.int32), (slots, "slots", (Bsz,), torch.int32),
+        (w, "w", (Ch, K), f32), (A, "A", (H,), f32), (bias, "bias", (Ch,), f32),
+        (D, "D", (H,), f32), (dt_bias, "dt_bias", (H,), f32), (y, "y", (Bsz, H, P), y_dtype))
+    ldx, lddt = _lead(xbc, "xbc"), _lead(dt, "dt")
+    with _scope(h, stream):
+        if y is None:
+            y = torch.empty((Bsz, H, P), dtype=y_dtype, device=h.device)
+            py = y.data_ptr()
+        _check(lib().ssd_mixer_step(ps, ph, pa, pm, nslots, xbc.data_ptr(), ldx, dt.data_ptr(), lddt,
+                                    pw, pi, int(act), pA, pD, pt, dt_min, dt_max, py, yd, Bsz, H, P,
+                                    G, N, K, code, _stream(stream)))
+    return y

@@ -780,3 +780,340 @@ int ssd_mimo_fwd(const void* y, int y_dtype, const void* W, void* z, int z_dtype
 }
 
 }  // extern "C"
+
+// ---- the layer's operators around the scan: norms, conv backward, fused step ----
+
+namespace {
+
+constexpr int kMaxNormSegment = 16384;  // channels of one norm: a row held in registers
+
+int check_dtype(int dtype, const char* name) {
+  if (dtype != SSD_F32 && dtype != SSD_BF16)
+    return fail(SSD_EUNSUPPORTED, "%s=%d is neither SSD_F32 nor SSD_BF16", name, dtype);
+  return SSD_OK;
+}
+
+size_t dsize(int dtype) { return dtype == SSD_BF16 ? 2 : 4; }
+
+int check_norm(int M, int D, int groups, float eps) {
+  if (M < 0 || D <= 0 || groups <= 0)
+    return fail(SSD_EINVAL, "need M >= 0, D > 0, groups > 0 (got M=%d D=%d groups=%d)", M, D, groups);
+  if (D % groups != 0) return fail(SSD_EINVAL, "D=%d is not a multiple of groups=%d", D, groups);
+  if (D / groups > kMaxNormSegment)
+    return fail(SSD_EUNSUPPORTED, "%d channels in one norm, at most %d", D / groups, kMaxNormSegment);
+  if (groups > 65535 || D > (1 << 24))
+    return fail(SSD_EUNSUPPORTED, "groups=%d above 65535 or D=%d above 2^24", groups, D);
+  if (!(eps >= 0.0f) || !(eps <= 3.0e38f)) return fail(SSD_EINVAL, "eps=%g must be finite and >= 0", eps);
+  return SSD_OK;
+}
+
+// Whether M rows of na bytes, lda apart, share a byte with M rows of nb bytes,
+// ldb apart (rows of equal pitch may interleave: columns of one wide row).
+bool rows_overlap(const void* a, size_t lda, size_t na, const void* b, size_t ldb, size_t nb, size_t M) {
+  if (!a || !b || M == 0) return false;
+  if (!overlaps(a, (M - 1) * lda + na, b, (M - 1) * ldb + nb)) return false;
+  if (lda != ldb || M == 1) return true;
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  const size_t d = y >= x ? (y - x) % lda : (lda - (x - y) % lda) % lda;  // b's column in a's rows
+  return d < na || d + nb > lda;
+}
+
+// one array of a call: `rows` rows of `bytes`, `pitch` apart; out: written
+struct Arr {
+  const void* p;
+  const char* name;
+  size_t pitch, bytes, rows;
+  bool out;
+};
+
+// No output may share memory with another array of the call, except for a
+// pair of equal `may` entries (an update in place).
+int check_overlap(const Arr* v, int n, const void* may = nullptr) {
+  for (int i = 0; i < n; ++i)
+    for (int j = i + 1; j < n; ++j) {
+      if (!v[i].out && !v[j].out) continue;
+      if (may && v[i].p == may && v[j].p == may && v[i].pitch == v[j].pitch) continue;
+      const bool hit =
+          v[i].rows == v[j].rows
+              ? rows_overlap(v[i].p, v[i].pitch, v[i].bytes, v[j].p, v[j].pitch, v[j].bytes, v[i].rows)
+              : v[i].rows && v[j].rows &&
+                    overlaps(v[i].p, (v[i].rows - 1) * v[i].pitch + v[i].bytes, v[j].p,
+                             (v[j].rows - 1) * v[j].pitch + v[j].bytes);
+      if (hit) return fail(SSD_EINVAL, "%s and %s overlap", v[i].name, v[j].name);
+    }
+  return SSD_OK;
+}
+
+size_t round_ws(size_t bytes) { return bytes ? (bytes + 255) / 256 * 256 : 256; }
+
+int check_workspace(const void* ws, size_t have, size_t need) {
+  if (!ws || have < need) return fail(SSD_EWORKSPACE, "workspace has %zu bytes, needs %zu", ws ? have : 0, need);
+  return check_ptr(ws, "workspace", 256, true);
+}
+
+}  // namespace
+
+extern "C" {
+
+int ssd_add_norm_fwd(const void* x, const float* scale, const void* residual, const float* w,
+                     float eps, void* residual_out, void* out, int M, int D, int x_dtype,
+                     int res_dtype, int out_dtype, void* stream) {
+  SSD_TRY(check_norm(M, D, 1, eps));
+  SSD_TRY(check_dtype(x_dtype, "x_dtype"));
+  SSD_TRY(check_dtype(res_dtype, "res_dtype"));
+  SSD_TRY(check_dtype(out_dtype, "out_dtype"));
+  const bool rows = M > 0;
+  const size_t xs = dsize(x_dtype), rs = dsize(res_dtype), os = dsize(out_dtype), d = D;
+  SSD_TRY(check_ptr(x, "x", xs, rows));
+  SSD_TRY(check_ptr(scale, "scale", 4, false));
+  SSD_TRY(check_ptr(residual, "residual", rs, false));
+  SSD_TRY(check_ptr(w, "w", 4, true));
+  SSD_TRY(check_ptr(residual_out, "residual_out", rs, false));
+  SSD_TRY(check_ptr(out, "out", os, rows));
+  const size_t m = M;
+  const Arr arrs[] = {{out, "out", d * os, d * os, m, true},
+                      {residual_out, "residual_out", d * rs, d * rs, m, true},
+                      {residual, "residual", d * rs, d * rs, m, false},
+                      {x, "x", d * xs, d * xs, m, false},
+                      {w, "w", d * 4, d * 4, 1, false},
+                      {scale, "scale", d * 4, d * 4, 1, false}};
+  SSD_TRY(check_overlap(arrs, 6, residual_out == residual ? residual : nullptr));
+  if (!rows) return ok();
+  ssd::AddNormArgs a{};
+  a.x = x, a.scale = scale, a.residual = residual, a.w = w, a.eps = eps, a.r_out = residual_out;
+  a.out = out, a.M = M, a.D = D, a.x_dtype = x_dtype, a.res_dtype = res_dtype, a.out_dtype = out_dtype;
+  return launch_status(ssd::run_add_norm(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t ssd_add_norm_bwd_workspace_size(int M, int D) {
+  if (check_norm(M, D, 1, 0.0f) != SSD_OK) return 0;
+  return round_ws(static_cast<size_t>(ssd::add_norm_parts(M, D)) * 2 * D * 4);
+}
+
+int ssd_add_norm_bwd(const void* dout, const void* dres, const void* r, const void* x,
+                     const float* scale, const float* w, float eps, void* dresidual, void* dx,
+                     float* dw, float* dscale, int M, int D, int x_dtype, int res_dtype,
+                     int out_dtype, void* workspace, size_t workspace_bytes, void* stream) {
+  SSD_TRY(check_norm(M, D, 1, eps));
+  SSD_TRY(check_dtype(x_dtype, "x_dtype"));
+  SSD_TRY(check_dtype(res_dtype, "res_dtype"));
+  SSD_TRY(check_dtype(out_dtype, "out_dtype"));
+  const bool rows = M > 0;
+  const size_t xs = dsize(x_dtype), rs = dsize(res_dtype), os = dsize(out_dtype), d = D, m = M;
+  SSD_TRY(check_ptr(dout, "dout", os, rows));
+  SSD_TRY(check_ptr(dres, "dres", rs, false));
+  SSD_TRY(check_ptr(r, "r", rs, rows));
+  SSD_TRY(check_ptr(x, "x", xs, rows && dscale));
+  SSD_TRY(check_ptr(scale, "scale", 4, false));
+  SSD_TRY(check_ptr(w, "w", 4, true));
+  SSD_TRY(check_ptr(dresidual, "dresidual", rs, false));
+  SSD_TRY(check_ptr(dx, "dx", xs, false));
+  SSD_TRY(check_ptr(dw, "dw", 4, true));
+  SSD_TRY(check_ptr(dscale, "dscale", 4, false));
+  const size_t need = ssd_add_norm_bwd_workspace_size(M, D);
+  SSD_TRY(check_workspace(workspace, workspace_bytes, need));
+  const Arr arrs[] = {{dresidual, "dresidual", d * rs, d * rs, m, true},
+                      {dx, "dx", d * xs, d * xs, m, true},
+                      {dw, "dw", d * 4, d * 4, 1, true},
+                      {dscale, "dscale", d * 4, d * 4, 1, true},
+                      {workspace, "workspace", need, need, 1, true},
+                      {dout, "dout", d * os, d * os, m, false},
+                      {dres, "dres", d * rs, d * rs, m, false},
+                      {r, "r", d * rs, d * rs, m, false},
+                      {x, "x", d * xs, d * xs, m, false},
+                      {scale, "scale", d * 4, d * 4, 1, false},
+                      {w, "w", d * 4, d * 4, 1, false}};
+  SSD_TRY(check_overlap(arrs, 11));
+  ssd::AddNormArgs a{};
+  a.dout = dout, a.dres = dres, a.r = r, a.x = x, a.scale = scale, a.w = w, a.eps = eps;
+  a.dresidual = dresidual, a.dx = dx, a.dw = dw, a.dscale = dscale, a.M = M, a.D = D;
+  a.x_dtype = x_dtype, a.res_dtype = res_dtype, a.out_dtype = out_dtype, a.workspace = workspace;
+  return launch_status(ssd::run_add_norm_bwd(a, static_cast<hipStream_t>(stream)));
+}
+
+int ssd_gated_norm_fwd(const void* y, const void* z, long long ldz, const float* w, float eps,
+                       int norm_before_gate, void* out, int M, int D, int groups, int y_dtype,
+                       int z_dtype, int out_dtype, void* stream) {
+  SSD_TRY(check_norm(M, D, groups, eps));
+  SSD_TRY(check_dtype(y_dtype, "y_dtype"));
+  SSD_TRY(check_dtype(z_dtype, "z_dtype"));
+  SSD_TRY(check_dtype(out_dtype, "out_dtype"));
+  if (norm_before_gate != 0 && norm_before_gate != 1)
+    return fail(SSD_EINVAL, "norm_before_gate=%d not in {0, 1}", norm_before_gate);
+  if (ldz < D || ldz > (1LL << 40)) return fail(SSD_EINVAL, "ldz=%lld not in [D=%d, 2^40]", ldz, D);
+  const bool rows = M > 0;
+  const size_t ys = dsize(y_dtype), zs = dsize(z_dtype), os = dsize(out_dtype), d = D, m = M;
+  SSD_TRY(check_ptr(y, "y", ys, rows));
+  SSD_TRY(check_ptr(z, "z", zs, rows));
+  SSD_TRY(check_ptr(w, "w", 4, true));
+  SSD_TRY(check_ptr(out, "out", os, rows));
+  const Arr arrs[] = {{out, "out", d * os, d * os, m, true},
+                      {y, "y", d * ys, d * ys, m, false},
+                      {z, "z", static_cast<size_t>(ldz) * zs, d * zs, m, false},
+                      {w, "w", d * 4, d * 4, 1, false}};
+  SSD_TRY(check_overlap(arrs, 4));
+  if (!rows) return ok();
+  ssd::GatedNormArgs a{};
+  a.y = y, a.z = z, a.ldz = ldz, a.w = w, a.eps = eps, a.before = norm_before_gate, a.out = out;
+  a.M = M, a.D = D, a.groups = groups, a.y_dtype = y_dtype, a.z_dtype = z_dtype, a.out_dtype = out_dtype;
+  return launch_status(ssd::run_gated_norm(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t ssd_gated_norm_bwd_workspace_size(int M, int D, int groups) {
+  if (check_norm(M, D, groups, 0.0f) != SSD_OK) return 0;
+  return round_ws(static_cast<size_t>(ssd::gated_norm_parts(M, D, groups)) * D * 4);
+}
+
+int ssd_gated_norm_bwd(const void* dout, const void* y, const void* z, long long ldz, const float* w,
+                       float eps, int norm_before_gate, void* dy, void* dz, long long lddz, float* dw,
+                       int M, int D, int groups, int y_dtype, int z_dtype, int out_dtype,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  SSD_TRY(check_norm(M, D, groups, eps));
+  SSD_TRY(check_dtype(y_dtype, "y_dtype"));
+  SSD_TRY(check_dtype(z_dtype, "z_dtype"));
+  SSD_TRY(check_dtype(out_dtype, "out_dtype"));
+  if (norm_before_gate != 0 && norm_before_gate != 1)
+    return fail(SSD_EINVAL, "norm_before_gate=%d not in {0, 1}", norm_before_gate);
+  if (ldz < D || ldz > (1LL << 40)) return fail(SSD_EINVAL, "ldz=%lld not in [D=%d, 2^40]", ldz, D);
+  if (lddz < D || lddz > (1LL << 40)) return fail(SSD_EINVAL, "lddz=%lld not in [D=%d, 2^40]", lddz, D);
+  const bool rows = M > 0;
+  const size_t ys = dsize(y_dtype), zs = dsize(z_dtype), os = dsize(out_dtype), d = D, m = M;
+  SSD_TRY(check_ptr(dout, "dout", os, rows));
+  SSD_TRY(check_ptr(y, "y", ys, rows));
+  SSD_TRY(check_ptr(z, "z", zs, rows));
+  SSD_TRY(check_ptr(w, "w", 4, true));
+  SSD_TRY(check_ptr(dy, "dy", ys, rows));
+  SSD_TRY(check_ptr(dz, "dz", zs, rows));
+  SSD_TRY(check_ptr(dw, "dw", 4, true));
+  const size_t need = ssd_gated_norm_bwd_workspace_size(M, D, groups);
+  SSD_TRY(check_workspace(workspace, workspace_bytes, need));
+  const Arr arrs[] = {{dy, "dy", d * ys, d * ys, m, true},
+                      {dz, "dz", static_cast<size_t>(lddz) * zs, d * zs, m, true},
+                      {dw, "dw", d * 4, d * 4, 1, true},
+                      {workspace, "workspace", need, need, 1, true},
+                      {dout, "dout", d * os, d * os, m, false},
+                      {y, "y", d * ys, d * ys, m, false},
+                      {z, "z", static_cast<size_t>(ldz) * zs, d * zs, m, false},
+                      {w, "w", d * 4, d * 4, 1, false}};
+  SSD_TRY(check_overlap(arrs, 8));
+  ssd::GatedNormArgs a{};
+  a.y = y, a.z = z, a.ldz = ldz, a.w = w, a.eps = eps, a.before = norm_before_gate, a.dout = dout;
+  a.dy = dy, a.dz = dz, a.lddz = lddz, a.dw = dw, a.M = M, a.D = D, a.groups = groups;
+  a.y_dtype = y_dtype, a.z_dtype = z_dtype, a.out_dtype = out_dtype, a.workspace = workspace;
+  return launch_status(ssd::run_gated_norm_bwd(a, static_cast<hipStream_t>(stream)));
+}
+
+size_t ssd_conv1d_bwd_workspace_size(int Bsz, int T, int HP, int GN) {
+  if (Bsz <= 0 || T < 0 || HP <= 0 || GN < 0 || T > (1 << 30)) return 0;
+  const size_t Ch = static_cast<size_t>(HP) + 2 * static_cast<size_t>(GN);
+  if (Ch > (1u << 24)) return 0;
+  return round_ws(static_cast<size_t>(ssd::conv_bwd_parts(Bsz, T)) * 5 * Ch * 4);
+}
+
+int ssd_conv1d_bwd(const void* xbc, long long ld, const float* w, const float* bias,
+                   const float* state_in, int act, const void* dx, const float* dB, const float* dC,
+                   const float* dstate_out, void* dxbc, long long lddx, float* dw, float* dbias,
+                   float* dstate_in, int Bsz, int T, int HP, int GN, int K, int dtype,
+                   void* workspace, size_t workspace_bytes, void* stream) {
+  SSD_TRY(check_dtype(dtype, "dtype"));
+  const int V = dtype == SSD_BF16 ? 8 : 4;
+  if (T < 0) return fail(SSD_EINVAL, "T=%d is negative", T);
+  SSD_TRY(check_conv_common(Bsz, HP, GN, ld, K, act, V));
+  SSD_TRY(check_conv_common(Bsz, HP, GN, lddx, K, act, V));
+  if (T > (1 << 30)) return fail(SSD_EUNSUPPORTED, "T=%d above 2^30", T);
+  const size_t Ch = static_cast<size_t>(HP) + 2 * static_cast<size_t>(GN);
+  if (Ch > (1u << 24)) return fail(SSD_EUNSUPPORTED, "%zu channels, at most 2^24", Ch);
+  const bool has_tokens = T > 0;
+  SSD_TRY(check_ptr(xbc, "xbc", 16, has_tokens));
+  SSD_TRY(check_ptr(w, "w", 16, true));
+  SSD_TRY(check_ptr(bias, "bias", 16, false));
+  SSD_TRY(check_ptr(state_in, "state_in", 16, false));
+  SSD_TRY(check_ptr(dx, "dx", 16, has_tokens));
+  SSD_TRY(check_ptr(dB, "dB", 16, has_tokens && GN > 0));
+  SSD_TRY(check_ptr(dC, "dC", 16, has_tokens && GN > 0));
+  SSD_TRY(check_ptr(dstate_out, "dstate_out", 16, false));
+  SSD_TRY(check_ptr(dxbc, "dxbc", 16, has_tokens));
+  SSD_TRY(check_ptr(dw, "dw", 16, true));
+  SSD_TRY(check_ptr(dbias, "dbias", 16, true));
+  SSD_TRY(check_ptr(dstate_in, "dstate_in", 16, false));
+  const size_t need = ssd_conv1d_bwd_workspace_size(Bsz, T, HP, GN);
+  SSD_TRY(check_workspace(workspace, workspace_bytes, need));
+  const size_t es = dsize(dtype), rows = static_cast<size_t>(Bsz) * T, sb = 3 * Ch * 4, nb = Bsz;
+  const Arr arrs[] = {{dxbc, "dxbc", static_cast<size_t>(lddx) * es, Ch * es, rows, true},
+                      {dw, "dw", Ch * 16, Ch * 16, 1, true},
+                      {dbias, "dbias", Ch * 4, Ch * 4, 1, true},
+                      {dstate_in, "dstate_in", sb, sb, nb, true},
+                      {workspace, "workspace", need, need, 1, true},
+                      {xbc, "xbc", static_cast<size_t>(ld) * es, Ch * es, rows, false},
+                      {dx, "dx", HP * es, HP * es, rows, false},
+                      {dB, "dB", GN * size_t{4}, GN * size_t{4}, GN ? rows : 0, false},
+                      {dC, "dC", GN * size_t{4}, GN * size_t{4}, GN ? rows : 0, false},
+                      {state_in, "state_in", sb, sb, nb, false},
+                      {dstate_out, "dstate_out", sb, sb, nb, false},
+                      {w, "w", Ch * 16, Ch * 16, 1, false},
+                      {bias, "bias", Ch * 4, Ch * 4, 1, false}};
+  SSD_TRY(check_overlap(arrs, 13));
+  ssd::ConvBwdArgs a{xbc,  ld,    w,         bias, state_in, act, dx, dB,    dC,       dstate_out, dxbc,
+                     lddx, dw,    dbias,     dstate_in, Bsz, T,   HP, GN,    dtype,    workspace};
+  return launch_status(ssd::run_conv1d_bwd(a, static_cast<hipStream_t>(stream)));
+}
+
+int ssd_mixer_step(float* conv_state, float* h, int* arrivals, const int* slots, int nslots,
+                   const void* xbc, long long ldx, const void* dt, long long lddt, const float* w,
+                   const float* bias, int act, const float* A, const float* D, const float* dt_bias,
+                   float dt_min, float dt_max, void* y, int y_dtype, int Bsz, int H, int P, int G,
+                   int N, int K, int dtype, void* stream) {
+  SSD_TRY(check_dtype(dtype, "dtype"));
+  SSD_TRY(check_dtype(y_dtype, "y_dtype"));
+  if (Bsz < 0 || nslots <= 0 || H <= 0 || P <= 0 || G <= 0 || N <= 0)
+    return fail(SSD_EINVAL, "sizes must be positive (Bsz >= 0): Bsz=%d nslots=%d H=%d P=%d G=%d N=%d", Bsz,
+                nslots, H, P, G, N);
+  if (H % G != 0) return fail(SSD_EINVAL, "H=%d is not a multiple of G=%d", H, G);
+  if (!in_set(N, kNsDecode, 5)) return fail(SSD_EUNSUPPORTED, "N=%d not in {16,32,64,128,256}", N);
+  if (P > 1024) return fail(SSD_EUNSUPPORTED, "P=%d above 1024", P);
+  if (K != 4) return fail(SSD_EUNSUPPORTED, "K=%d: only kernel size 4 is built", K);
+  if (act != 0 && act != 1) return fail(SSD_EINVAL, "act=%d not in {0, 1}", act);
+  if (!slots && Bsz > nslots)
+    return fail(SSD_EINVAL, "Bsz=%d rows without a slot map, nslots=%d", Bsz, nslots);
+  if (static_cast<long long>(Bsz) * H > 2147483647LL) return fail(SSD_EUNSUPPORTED, "Bsz*H too large");
+  const size_t Ch = static_cast<size_t>(H) * P + 2 * static_cast<size_t>(G) * N;
+  if (Ch > (1u << 24)) return fail(SSD_EUNSUPPORTED, "%zu channels, at most 2^24", Ch);
+  if (ldx < static_cast<long long>(Ch) || ldx > (1LL << 40))
+    return fail(SSD_EINVAL, "ldx=%lld not in [%zu, 2^40]", ldx, Ch);
+  if (lddt < H || lddt > (1LL << 40)) return fail(SSD_EINVAL, "lddt=%lld not in [%d, 2^40]", lddt, H);
+  SSD_TRY(check_clamp(dt_min, dt_max));
+  const bool has = Bsz > 0;
+  const size_t es = dsize(dtype), ys = dsize(y_dtype), hp = static_cast<size_t>(H) * P;
+  SSD_TRY(check_ptr(conv_state, "conv_state", 4, true));
+  SSD_TRY(check_ptr(h, "h", 16, true));
+  SSD_TRY(check_ptr(arrivals, "arrivals", 4, H != G));
+  SSD_TRY(check_ptr(slots, "slots", 4, false));
+  SSD_TRY(check_ptr(xbc, "xbc", es, has));
+  SSD_TRY(check_ptr(dt, "dt", es, has));
+  SSD_TRY(check_ptr(w, "w", 16, true));
+  SSD_TRY(check_ptr(bias, "bias", 4, false));
+  SSD_TRY(check_ptr(A, "A", 4, true));
+  SSD_TRY(check_ptr(D, "D", 4, false));
+  SSD_TRY(check_ptr(dt_bias, "dt_bias", 4, false));
+  SSD_TRY(check_ptr(y, "y", ys, has));
+  const size_t n = nslots, b = Bsz, hb = static_cast<size_t>(H) * 4;
+  const Arr arrs[] = {{conv_state, "conv_state", 12 * Ch, 12 * Ch, n, true},
+                      {h, "h", hp * N * 4, hp * N * 4, n, true},
+                      {arrivals, "arrivals", G * size_t{4}, G * size_t{4}, n, true},
+                      {y, "y", hp * ys, hp * ys, b, true},
+                      {slots, "slots", 4, 4, b, false},
+                      {xbc, "xbc", static_cast<size_t>(ldx) * es, Ch * es, b, false},
+                      {dt, "dt", static_cast<size_t>(lddt) * es, H * es, b, false},
+                      {w, "w", Ch * 16, Ch * 16, 1, false},
+                      {bias, "bias", Ch * 4, Ch * 4, 1, false},
+                      {A, "A", hb, hb, 1, false},
+                      {D, "D", hb, hb, 1, false},
+                      {dt_bias, "dt_bias", hb, hb, 1, false}};
+  SSD_TRY(check_overlap(arrs, 12));
+  if (!has) return ok();
+  ssd::MixerStepArgs a{conv_state, h, reinterpret_cast<unsigned*>(arrivals), slots, nslots, xbc, ldx, dt,
+                       lddt, w, bias, act, A, D, dt_bias, dt_min, dt_max, y, y_dtype, Bsz, H, P, G, N, dtype};
+  return launch_status(ssd::run_mixer_step(a, static_cast<hipStream_t>(stream)));
+}
+
+}  // extern "C"

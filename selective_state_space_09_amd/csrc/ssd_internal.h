@@ -88,6 +88,83 @@ struct LinearArgs {
   hipEvent_t* events;   // NULL, or start/stop of the kernel
 };
 
+struct AddNormArgs {
+  const void* x;         // (M, D)
+  const float* scale;    // (D) or NULL
+  const void* residual;  // forward: (M, D) or NULL
+  const float* w;        // (D)
+  float eps;
+  void* r_out;           // forward: (M, D) or NULL
+  void* out;             // forward: (M, D)
+  const void* dout;      // backward from here on: (M, D)
+  const void* dres;      // (M, D) or NULL
+  const void* r;         // (M, D), the forward's r_out
+  void* dresidual;       // (M, D) or NULL
+  void* dx;              // (M, D) or NULL
+  float* dw;             // (D)
+  float* dscale;         // (D) or NULL
+  int M, D, x_dtype, res_dtype, out_dtype;
+  void* workspace;       // add_norm_parts(M, D) rows of 2 D floats
+};
+
+struct GatedNormArgs {
+  const void* y;         // (M, D)
+  const void* z;         // M rows of D elements, ldz apart
+  long long ldz;
+  const float* w;        // (D)
+  float eps;
+  int before;            // 1: the norm comes before the gate
+  void* out;             // forward: (M, D)
+  const void* dout;      // backward from here on: (M, D)
+  void* dy;              // (M, D)
+  void* dz;              // M rows of D elements, lddz apart
+  long long lddz;
+  float* dw;             // (D)
+  int M, D, groups, y_dtype, z_dtype, out_dtype;
+  void* workspace;       // gated_norm_parts(M, D, groups) rows of D floats
+};
+
+struct ConvBwdArgs {
+  const void* xbc;         // (Bsz, T, ld) rows
+  long long ld;
+  const float* w;          // (Ch, 4)
+  const float* bias;       // (Ch) or NULL
+  const float* state_in;   // (Bsz, 3, Ch) or NULL
+  int act;
+  const void* dx;          // (Bsz, T, HP), gradient of the output x
+  const float* dB;         // (Bsz, T, GN)
+  const float* dC;         // (Bsz, T, GN)
+  const float* dstate_out; // (Bsz, 3, Ch) or NULL
+  void* dxbc;              // (Bsz, T, lddx) rows
+  long long lddx;
+  float* dw;               // (Ch, 4)
+  float* dbias;            // (Ch)
+  float* dstate_in;        // (Bsz, 3, Ch) or NULL
+  int Bsz, T, HP, GN, dtype;
+  void* workspace;         // conv_bwd_parts(Bsz, T) rows of 5 Ch floats
+};
+
+struct MixerStepArgs {
+  float* conv;             // (nslots, 3, Ch)
+  float* h;                // (nslots, H, P, N)
+  unsigned* arrivals;      // (nslots, G), or NULL where H == G
+  const int* slots;        // (Bsz) or NULL (row b has slot b)
+  int nslots;
+  const void* xbc;         // Bsz rows of Ch elements, ldx apart
+  long long ldx;
+  const void* dt;          // Bsz rows of H elements, lddt apart
+  long long lddt;
+  const float* w;
+  const float* bias;
+  int act;
+  const float* A;
+  const float* D;
+  const float* dt_bias;
+  float dt_min, dt_max;
+  void* y;                 // (Bsz, H, P)
+  int y_dtype, Bsz, H, P, G, N, dtype;
+};
+
 // floats of chunk-boundary states: (Bsz, nc, H, P, KC), KC = N or 2N
 inline size_t workspace_state_floats(int Bsz, int nc, int H, int P, int KC) {
   return static_cast<size_t>(Bsz) * nc * H * P * KC;
@@ -248,5 +325,15 @@ hipError_t run_conv1d(const ConvArgs& a, hipStream_t st);
 hipError_t run_linear(const LinearArgs& a, hipStream_t st);  // K % 64 == 0, Nout % 128 == 0
 hipError_t run_conv1d_step(const ConvArgs& a, hipStream_t st);  // float32, T = 1
 int conv_tokens_per_thread();
+hipError_t run_add_norm(const AddNormArgs& a, hipStream_t st);
+hipError_t run_add_norm_bwd(const AddNormArgs& a, hipStream_t st);
+hipError_t run_gated_norm(const GatedNormArgs& a, hipStream_t st);
+hipError_t run_gated_norm_bwd(const GatedNormArgs& a, hipStream_t st);
+hipError_t run_conv1d_bwd(const ConvBwdArgs& a, hipStream_t st);
+hipError_t run_mixer_step(const MixerStepArgs& a, hipStream_t st);
+// rows of the partial-sum tables of the backward passes
+int add_norm_parts(int M, int D);
+int gated_norm_parts(int M, int D, int groups);
+int conv_bwd_parts(int Bsz, int T);
 
 }  // namespace ssd

@@ -1,0 +1,493 @@
+// RMS norms around the scan of a Mamba-2 block on gfx950.
+//
+// Before a block (pre-norm with the residual update; Mamba-3-Lite block page:
+// RMSNorm, pre-norm, eps 1e-5):
+//   r = residual + scale o x
+//   out = r rsqrt(mean(r^2) + eps) o w
+// and its gradient at the given r, with n = r rstd, dn = dout o w:
+//   g = dres + rstd (dn - n mean(dn o n))
+//   dresidual = g, dx = scale o g, dw = sum_rows dout o n, dscale = sum_rows g o x
+//
+// After the scan (the Mamba-2 layer's norm between the scan and out_proj), per
+// group of L = D / groups channels, s = silu(z):
+//   out = rms(y o s) o w            or, norm_before_gate,  rms(y) o w o s
+// with its gradient.
+//
+// All of it streams: about 10 flops per element against 6 to 18 bytes, so HBM
+// bounds it.  A team of TPR lanes owns a row segment and holds it in registers
+// (K vectors of 8 elements per lane), so every input is read once: one pass
+// for the sum of squares and, from the registers, the normalised values.  The
+// sums over rows (dw, dscale) stay in registers while a team walks its rows;
+// teams of a workgroup join them in LDS and write one row of a partial-sum
+// table, which a second kernel adds up in a fixed order.
+
+#include "ssd_chunk_common.h"
+#include "ssd_internal.h"
+#include "ssd_rows.h"
+
+namespace ssd {
+
+namespace {
+
+__device__ __forceinline__ float fast_sigmoid(float v) {
+  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.4426950408889634f));
+}
+
+// Sums of NV values per thread over a team of TPR lanes, returned in every
+// lane.  Teams wider than a wave go through LDS (red: 2 x 16 x NV floats,
+// alternating between calls, so that one barrier a call is enough).
+template <int TPR, int NV>
+__device__ __forceinline__ void team_sum(float (&v)[NV], float* red, int parity) {
+  constexpr int W = TPR < kWave ? TPR : kWave;
+#pragma unroll
+  for (int o = W / 2; o > 0; o >>= 1)
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] += __shfl_xor(v[i], o, kWave);
+  if constexpr (TPR > kWave) {
+    constexpr int NW = TPR / kWave;
+    float* slot = red + parity * 16 * NV;
+    if ((threadIdx.x & (kWave - 1)) == 0)
+#pragma unroll
+      for (int i = 0; i < NV; ++i) slot[(threadIdx.x / kWave) * NV + i] = v[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      float s = 0.0f;
+#pragma unroll
+      for (int k = 0; k < NW; ++k) s += slot[k * NV + i];
+      v[i] = s;
+    }
+  }
+}
+
+template <int TPR>
+constexpr int team_block() {
+  return TPR > kThreads ? TPR : kThreads;
+}
+
+template <int TPR, int K, typename TX, typename TR, typename TO>
+__global__ __launch_bounds__(team_block<TPR>()) void ssd_add_norm_kernel(
+    const TX* __restrict__ x, const float* __restrict__ scale, const TR* residual,
+    const float* __restrict__ w, float eps, TR* r_out, TO* __restrict__ out, int M, int D) {
+  constexpr int BT = team_block<TPR>(), TEAMS = BT / TPR;
+  __shared__ float red[TPR > kWave ? 32 : 1];
+  const int lane = threadIdx.x % TPR;
+  const float inv = 1.0f / static_cast<float>(D);
+  int parity = 0;
+  for (long long row = static_cast<long long>(blockIdx.x) * TEAMS + threadIdx.x / TPR; row < M;
+       row += static_cast<long long>(gridDim.x) * TEAMS) {
+    const size_t base = static_cast<size_t>(row) * D;
+    float r[K][8];
+    float ss[1] = {0.0f};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int v = lane + k * TPR;
+      const Row8<TX> xv = row_load(x + base, v, D);
+      Row8<float> sv;
+      Row8<TR> rv;
+      rv.zero();
+      if (scale) sv = row_load(scale, v, D);
+      if (residual) rv = row_load(residual + base, v, D);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        r[k][i] = scale ? fmaf(sv[i], xv[i], rv[i]) : xv[i] + rv[i];
+        ss[0] = fmaf(r[k][i], r[k][i], ss[0]);
+      }
+    }
+    team_sum<TPR, 1>(ss, red, parity);
+    parity ^= 1;
+    const float rstd = rsqrtf(ss[0] * inv + eps);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int v = lane + k * TPR;
+      const Row8<float> wv = row_load(w, v, D);
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = r[k][i] * rstd * wv[i];
+      if (r_out) row_store(r_out + base, v, D, r[k]);
+      row_store(out + base, v, D, o);
+    }
+  }
+}
+
+// The team's column sums (K vectors of 8 per lane) joined over the workgroup's
+// teams and written as columns col0 .. col0 + L - 1 of a partial row.
+template <int TPR, int K>
+__device__ __forceinline__ void write_part(const float (&acc)[K][8], float* buf, float* part, int L) {
+  constexpr int BT = team_block<TPR>(), TEAMS = BT / TPR;
+  const int lane = threadIdx.x % TPR;
+#pragma unroll
+  for (int k = 0; k < K; ++k) {
+    if constexpr (TEAMS > 1) {
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < 8; ++i) buf[threadIdx.x / TPR * (TPR * 8) + lane * 8 + i] = acc[k][i];
+      __syncthreads();
+      for (int j = threadIdx.x; j < TPR * 8; j += BT) {
+        float s = 0.0f;
+#pragma unroll
+        for (int t = 0; t < TEAMS; ++t) s += buf[t * (TPR * 8) + j];
+        const int col = k * TPR * 8 + j;
+        if (col < L) part[col] = s;
+      }
+    } else {
+      row_store(part, lane + k * TPR, L, acc[k]);
+    }
+  }
+}
+
+template <int TPR, int K, typename TX, typename TR, typename TO>
+__global__ __launch_bounds__(team_block<TPR>()) void ssd_add_norm_bwd_kernel(
+    const TO* __restrict__ dout, const TR* __restrict__ dres, const TR* __restrict__ r,
+    const TX* __restrict__ x, const float* __restrict__ scale, const float* __restrict__ w,
+    float eps, TR* __restrict__ dresidual, TX* __restrict__ dx, float* __restrict__ part, int M,
+    int D, int want_dscale) {
+  constexpr int BT = team_block<TPR>(), TEAMS = BT / TPR;
+  __shared__ float red[TPR > kWave ? 64 : 1];
+  __shared__ float buf[TEAMS > 1 ? BT * 8 : 1];
+  const int lane = threadIdx.x % TPR;
+  const float inv = 1.0f / static_cast<float>(D);
+  float dw[K][8] = {}, ds[K][8] = {};
+  int parity = 0;
+  for (long long row = static_cast<long long>(blockIdx.x) * TEAMS + threadIdx.x / TPR; row < M;
+       row += static_cast<long long>(gridDim.x) * TEAMS) {
+    const size_t base = static_cast<size_t>(row) * D;
+    Row8<TR> rv[K];
+    Row8<TO> dv[K];
+    float s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int v = lane + k * TPR;
+      rv[k] = row_load(r + base, v, D);
+      dv[k] = row_load(dout + base, v, D);
+      const Row8<float> wv = row_load(w, v, D);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        s[0] = fmaf(rv[k][i], rv[k][i], s[0]);
+        s[1] = fmaf(dv[k][i] * wv[i], rv[k][i], s[1]);
+      }
+    }
+    team_sum<TPR, 2>(s, red, parity);
+    parity ^= 1;
+    const float rstd = rsqrtf(s[0] * inv + eps);
+    const float m = s[1] * rstd * inv;  // mean(dn o n)
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int v = lane + k * TPR;
+      const Row8<float> wv = row_load(w, v, D);
+      Row8<TR> ev;
+      ev.zero();
+      if (dres) ev = row_load(dres + base, v, D);
+      float g[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float n = rv[k][i] * rstd;
+        dw[k][i] = fmaf(dv[k][i], n, dw[k][i]);
+        g[i] = fmaf(rstd, fmaf(-n, m, dv[k][i] * wv[i]), ev[i]);
+      }
+      if (dresidual) row_store(dresidual + base, v, D, g);
+      if (want_dscale) {
+        const Row8<TX> xv = row_load(x + base, v, D);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ds[k][i] = fmaf(g[i], xv[i], ds[k][i]);
+      }
+      if (dx) {
+        if (scale) {
+          const Row8<float> sv = row_load(scale, v, D);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) g[i] *= sv[i];
+        }
+        row_store(dx + base, v, D, g);
+      }
+    }
+  }
+  float* p = part + static_cast<size_t>(blockIdx.x) * (want_dscale ? 2 : 1) * D;
+  write_part<TPR, K>(dw, buf, p, D);
+  if (want_dscale) write_part<TPR, K>(ds, buf, p + D, D);
+}
+
+// Grid: x = row blocks, y = groups.
+template <int TPR, int K, typename TY, typename TZ, typename TO>
+__global__ __launch_bounds__(team_block<TPR>()) void ssd_gated_norm_kernel(
+    const TY* __restrict__ y, const TZ* __restrict__ z, long long ldz, const float* __restrict__ w,
+    float eps, int before, TO* __restrict__ out, int M, int D, int L) {
+  constexpr int BT = team_block<TPR>(), TEAMS = BT / TPR;
+  __shared__ float red[TPR > kWave ? 32 : 1];
+  const int lane = threadIdx.x % TPR;
+  const float inv = 1.0f / static_cast<float>(L);
+  const size_t c0 = static_cast<size_t>(blockIdx.y) * L;
+  int parity = 0;
+  for (long long row = static_cast<long long>(blockIdx.x) * TEAMS + threadIdx.x / TPR; row < M;
+       row += static_cast<long long>(gridDim.x) * TEAMS) {
+    const size_t base = static_cast<size_t>(row) * D + c0;
+    float u[K][8], gt[K][8];
+    float ss[1] = {0.0f};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int v = lane + k * TPR;
+      const Row8<TY> yv = row_load(y + base, v, L);
+      const Row8<TZ> zv = row_load(z + static_cast<size_t>(row) * ldz + c0, v, L);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float s = zv[i] * fast_sigmoid(zv[i]);
+        u[k][i] = before ? yv[i] : yv[i] * s;
+        gt[k][i] = before ? s : 1.0f;
+        ss[0] = fmaf(u[k][i], u[k][i], ss[0]);
+      }
+    }
+    team_sum<TPR, 1>(ss, red, parity);
+    parity ^= 1;
+    const float rstd = rsqrtf(ss[0] * inv + eps);
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int v = lane + k * TPR;
+      const Row8<float> wv = row_load(w + c0, v, L);
+      float o[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] = u[k][i] * rstd * wv[i] * gt[k][i];
+      row_store(out + base, v, L, o);
+    }
+  }
+}
+
+template <int TPR, int K, typename TY, typename TZ, typename TO>
+__global__ __launch_bounds__(team_block<TPR>()) void ssd_gated_norm_bwd_kernel(
+    const TO* __restrict__ dout, const TY* __restrict__ y, const TZ* __restrict__ z, long long ldz,
+    const float* __restrict__ w, float eps, int before, TY* __restrict__ dy, TZ* __restrict__ dz,
+    long long lddz, float* __restrict__ part, int M, int D, int L) {
+  constexpr int BT = team_block<TPR>(), TEAMS = BT / TPR;
+  __shared__ float red[TPR > kWave ? 64 : 1];
+  __shared__ float buf[TEAMS > 1 ? BT * 8 : 1];
+  const int lane = threadIdx.x % TPR;
+  const float inv = 1.0f / static_cast<float>(L);
+  const size_t c0 = static_cast<size_t>(blockIdx.y) * L;
+  float dw[K][8] = {};
+  int parity = 0;
+  for (long long row = static_cast<long long>(blockIdx.x) * TEAMS + threadIdx.x / TPR; row < M;
+       row += static_cast<long long>(gridDim.x) * TEAMS) {
+    const size_t base = static_cast<size_t>(row) * D + c0;
+    Row8<TY> yv[K];
+    Row8<TZ> zv[K];
+    Row8<TO> dv[K];
+    float s[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int v = lane + k * TPR;
+      yv[k] = row_load(y + base, v, L);
+      zv[k] = row_load(z + static_cast<size_t>(row) * ldz + c0, v, L);
+      dv[k] = row_load(dout + base, v, L);
+      const Row8<float> wv = row_load(w + c0, v, L);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float gate = zv[k][i] * fast_sigmoid(zv[k][i]);
+        const float u = before ? yv[k][i] : yv[k][i] * gate;
+        const float dn = before ? dv[k][i] * gate : dv[k][i];
+        s[0] = fmaf(u, u, s[0]);
+        s[1] = fmaf(dn * wv[i], u, s[1]);
+      }
+    }
+    team_sum<TPR, 2>(s, red, parity);
+    parity ^= 1;
+    const float rstd = rsqrtf(s[0] * inv + eps);
+    const float m = s[1] * rstd * inv;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int v = lane + k * TPR;
+      const Row8<float> wv = row_load(w + c0, v, L);
+      float gy[8], gz[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float zz = zv[k][i], sig = fast_sigmoid(zz), gate = zz * sig;
+        const float u = before ? yv[k][i] : yv[k][i] * gate;
+        const float n = u * rstd;
+        const float dn = before ? dv[k][i] * gate : dv[k][i];
+        dw[k][i] = fmaf(dn, n, dw[k][i]);
+        const float du = rstd * fmaf(-n, m, dn * wv[i]);
+        gy[i] = before ? du : du * gate;
+        const float dg = before ? dv[k][i] * n * wv[i] : du * yv[k][i];
+        gz[i] = dg * sig * fmaf(zz, 1.0f - sig, 1.0f);
+      }
+      row_store(dy + base, v, L, gy);
+      row_store(dz + static_cast<size_t>(row) * lddz + c0, v, L, gz);
+    }
+  }
+  write_part<TPR, K>(dw, buf, part + static_cast<size_t>(blockIdx.x) * D + c0, L);
+}
+
+// Grid: blocks of 64 columns; 4 waves split the parts.
+__global__ __launch_bounds__(kThreads) void ssd_sum_parts_kernel(const float* __restrict__ part,
+                                                                  int nparts, int n,
+                                                                  float* __restrict__ a, int na,
+                                                                  float* __restrict__ b) {
+  __shared__ float s[4][kWave];
+  const int lane = threadIdx.x & (kWave - 1), wv = threadIdx.x / kWave;
+  const int col = blockIdx.x * kWave + lane;
+  float acc = 0.0f;
+  if (col < n)
+    for (int p = wv; p < nparts; p += 4) acc += part[static_cast<size_t>(p) * n + col];
+  s[wv][lane] = acc;
+  __syncthreads();
+  if (wv == 0 && col < n) {
+    const float t = (s[0][lane] + s[1][lane]) + (s[2][lane] + s[3][lane]);
+    if (col < na)
+      a[col] = t;
+    else
+      b[col - na] = t;
+  }
+}
+
+// rows a team covers at once, by the (TPR, K) that a segment of L elements gets
+struct Shape {
+  int tpr, k;
+};
+Shape shape_of(int L) {
+  if (L <= 128) return {16, 1};
+  if (L <= 512) return {64, 1};
+  if (L <= 1024) return {64, 2};
+  if (L <= 2048) return {64, 4};
+  if (L <= 4096) return {256, 2};
+  if (L <= 8192) return {256, 4};
+  return {1024, 2};
+}
+
+int teams_of(int L) {
+  const int tpr = shape_of(L).tpr;
+  return tpr > kThreads ? 1 : kThreads / tpr;
+}
+
+// workgroups along the rows: enough for every row, at most `cap`
+int row_blocks(int M, int L, int groups, int cap) {
+  const int t = teams_of(L);
+  const long long need = (static_cast<long long>(M) + t - 1) / t;
+  const long long most = cap / groups > 0 ? cap / groups : 1;
+  return static_cast<int>(need < most ? need : most);
+}
+
+constexpr int kFwdBlocks = 4096;
+constexpr int kBwdBlocks = 1024;
+
+#define SSD_ROW_SHAPES(L, CASE)              \
+  switch (shape_of(L).tpr * 8 + shape_of(L).k) { \
+    CASE(16, 1)                              \
+    CASE(64, 1)                              \
+    CASE(64, 2)                              \
+    CASE(64, 4)                              \
+    CASE(256, 2)                             \
+    CASE(256, 4)                             \
+    CASE(1024, 2)                            \
+    default:                                 \
+      return hipErrorInvalidValue;           \
+  }
+
+template <typename TX, typename TR, typename TO>
+hipError_t add_norm_fwd_t(const AddNormArgs& a, hipStream_t st) {
+  const dim3 grid(row_blocks(a.M, a.D, 1, kFwdBlocks));
+#define SSD_CASE(TPR, K)                                                                          \
+  case TPR * 8 + K:                                                                               \
+    launch_k(true, ssd_add_norm_kernel<TPR, K, TX, TR, TO>, grid, dim3(team_block<TPR>()), st,     \
+             nullptr, static_cast<const TX*>(a.x), a.scale, static_cast<const TR*>(a.residual),  \
+             a.w, a.eps, static_cast<TR*>(a.r_out), static_cast<TO*>(a.out), a.M, a.D);           \
+    break;
+  SSD_ROW_SHAPES(a.D, SSD_CASE)
+#undef SSD_CASE
+  return hipGetLastError();
+}
+
+template <typename TX, typename TR, typename TO>
+hipError_t add_norm_bwd_t(const AddNormArgs& a, hipStream_t st) {
+  const int nparts = row_blocks(a.M, a.D, 1, kBwdBlocks);
+  const dim3 grid(nparts);
+  float* part = static_cast<float*>(a.workspace);
+  if (nparts > 0)  // no rows: the sums are zero
+#define SSD_CASE(TPR, K)                                                                            \
+  case TPR * 8 + K:                                                                                 \
+    launch_k(true, ssd_add_norm_bwd_kernel<TPR, K, TX, TR, TO>, grid, dim3(team_block<TPR>()), st,   \
+             nullptr, static_cast<const TO*>(a.dout), static_cast<const TR*>(a.dres),               \
+             static_cast<const TR*>(a.r), static_cast<const TX*>(a.x), a.scale, a.w, a.eps,          \
+             static_cast<TR*>(a.dresidual), static_cast<TX*>(a.dx), part, a.M, a.D,                  \
+             static_cast<int>(a.dscale != nullptr));                                                 \
+    break;
+  SSD_ROW_SHAPES(a.D, SSD_CASE)
+#undef SSD_CASE
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return sum_parts(part, nparts, a.dscale ? 2 * a.D : a.D, a.dw, a.D, a.dscale, st);
+}
+
+template <typename TY, typename TZ, typename TO>
+hipError_t gated_norm_fwd_t(const GatedNormArgs& a, hipStream_t st) {
+  const int L = a.D / a.groups;
+  const dim3 grid(row_blocks(a.M, L, a.groups, kFwdBlocks), a.groups);
+#define SSD_CASE(TPR, K)                                                                          \
+  case TPR * 8 + K:                                                                               \
+    launch_k(true, ssd_gated_norm_kernel<TPR, K, TY, TZ, TO>, grid, dim3(team_block<TPR>()), st,   \
+             nullptr, static_cast<const TY*>(a.y), static_cast<const TZ*>(a.z), a.ldz, a.w,       \
+             a.eps, a.before, static_cast<TO*>(a.out), a.M, a.D, L);                               \
+    break;
+  SSD_ROW_SHAPES(L, SSD_CASE)
+#undef SSD_CASE
+  return hipGetLastError();
+}
+
+template <typename TY, typename TZ, typename TO>
+hipError_t gated_norm_bwd_t(const GatedNormArgs& a, hipStream_t st) {
+  const int L = a.D / a.groups;
+  const int nparts = row_blocks(a.M, L, a.groups, kBwdBlocks);
+  const dim3 grid(nparts, a.groups);
+  float* part = static_cast<float*>(a.workspace);
+  if (nparts > 0)  // no rows: the sums are zero
+#define SSD_CASE(TPR, K)                                                                            \
+  case TPR * 8 + K:                                                                                 \
+    launch_k(true, ssd_gated_norm_bwd_kernel<TPR, K, TY, TZ, TO>, grid, dim3(team_block<TPR>()), st, \
+             nullptr, static_cast<const TO*>(a.dout), static_cast<const TY*>(a.y),                  \
+             static_cast<const TZ*>(a.z), a.ldz, a.w, a.eps, a.before, static_cast<TY*>(a.dy),       \
+             static_cast<TZ*>(a.dz), a.lddz, part, a.M, a.D, L);                                     \
+    break;
+  SSD_ROW_SHAPES(L, SSD_CASE)
+#undef SSD_CASE
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  return sum_parts(part, nparts, a.D, a.dw, a.D, nullptr, st);
+}
+
+// the three element types of a call, each float32 (0) or bfloat16 (1)
+#define SSD_TYPES3(FN, a, t0, t1, t2, st)                            \
+  switch ((t0) * 4 + (t1) * 2 + (t2)) {                              \
+    case 0: return FN<float, float, float>(a, st);                   \
+    case 1: return FN<float, float, uint16_t>(a, st);                \
+    case 2: return FN<float, uint16_t, float>(a, st);                \
+    case 3: return FN<float, uint16_t, uint16_t>(a, st);             \
+    case 4: return FN<uint16_t, float, float>(a, st);                \
+    case 5: return FN<uint16_t, float, uint16_t>(a, st);             \
+    case 6: return FN<uint16_t, uint16_t, float>(a, st);             \
+    default: return FN<uint16_t, uint16_t, uint16_t>(a, st);         \
+  }
+
+}  // namespace
+
+hipError_t sum_parts(const float* part, int nparts, int n, float* a, int na, float* b,
+                     hipStream_t st) {
+  launch_k(true, ssd_sum_parts_kernel, dim3((n + kWave - 1) / kWave), dim3(kThreads), st, nullptr,
+           part, nparts, n, a, na, b);
+  return hipGetLastError();
+}
+
+int add_norm_parts(int M, int D) { return row_blocks(M, D, 1, kBwdBlocks); }
+int gated_norm_parts(int M, int D, int groups) {
+  return row_blocks(M, D / groups, groups, kBwdBlocks);
+}
+
+hipError_t run_add_norm(const AddNormArgs& a, hipStream_t st) {
+  SSD_TYPES3(add_norm_fwd_t, a, a.x_dtype, a.res_dtype, a.out_dtype, st)
+}
+hipError_t run_add_norm_bwd(const AddNormArgs& a, hipStream_t st) {
+  SSD_TYPES3(add_norm_bwd_t, a, a.x_dtype, a.res_dtype, a.out_dtype, st)
+}
+hipError_t run_gated_norm(const GatedNormArgs& a, hipStream_t st) {
+  SSD_TYPES3(gated_norm_fwd_t, a, a.y_dtype, a.z_dtype, a.out_dtype, st)
+}
+hipError_t run_gated_norm_bwd(const GatedNormArgs& a, hipStream_t st) {
+  SSD_TYPES3(gated_norm_bwd_t, a, a.y_dtype, a.z_dtype, a.out_dtype, st)
+}
+
+}  // namespace ssd
