@@ -801,8 +801,16 @@ def ssd_mimo_fwd(y, W, z=None, out_dtype=torch.bfloat16, stream=None):
     return z
 
 
-class _SameDevice:
-    """The scope of a call on the current device and stream: nothing to do."""
+_CODES = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16}
+
+
+def _code(dtype, name):
+    c = _CODES.get(dtype)
+    return _dcode(dtype, name) if c is None else c
+
+
+class _Here:
+    """The scope of a call on the current device and its current stream."""
 
     def __enter__(self):
         return None
@@ -811,7 +819,7 @@ class _SameDevice:
         return False
 
 
-_SAME_DEVICE = _SameDevice()
+_HERE_SCOPE = _Here()
 
 
 def _scope(t, stream):
@@ -822,15 +830,35 @@ def _scope(t, stream):
         if stream.device != t.device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
         return torch.cuda.stream(stream)
-    if t.device.index == torch.cuda.current_device():
-        return _SAME_DEVICE
+    if t.get_device() == torch._C._cuda_getDevice():
+        return _HERE_SCOPE
     return torch.cuda.device(t.device)
 
 
+def _raw_stream(t):
+    """Handle of the current stream of t's device (inside its _scope)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
 def _tensors(ref, *specs):
-    """Pointers of the arguments (tensor or None, name, shape, dtype): every
-    shape and type is checked before any device, each must be contiguous on
-    ref's GPU."""
+    """Pointers of the arguments (tensor or None, name, shape, dtype), each of
+    exactly this shape and type and contiguous on ref's GPU."""
+    out = []
+    dev = ref.get_device()
+    for t, name, shape, dtype in specs:
+        if t is None:
+            out.append(None)
+        elif (t.shape == shape and t.dtype is dtype and t.get_device() == dev and dev >= 0
+              and t.is_contiguous()):
+            out.append(t.data_ptr())
+        else:
+            _refuse(ref, specs)
+    return out
+
+
+def _refuse(ref, specs):
+    """Raises for the first argument that _tensors does not take: any shape or
+    type before any device or layout."""
     for t, name, shape, dtype in specs:
         if t is None:
             continue
@@ -838,20 +866,16 @@ def _tensors(ref, *specs):
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
         if t.dtype != dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    out = []
-    dev = ref.device
     for t, name, shape, dtype in specs:
         if t is None:
-            out.append(None)
             continue
         if not t.is_cuda:
             raise ValueError(f"{name} must be a GPU tensor")
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+        if t.device != ref.device:
+            raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        out.append(t.data_ptr())
-    return out
+    raise AssertionError("unreachable")
 
 
 def _rows_like(t, name, shape, dtype, ref):
@@ -860,7 +884,7 @@ def _rows_like(t, name, shape, dtype, ref):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != ref.device:
+    if t.get_device() != ref.get_device():
         raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
 
 
@@ -870,6 +894,8 @@ def _lead(t, name):
     stride in elements."""
     if not t.is_cuda:
         raise ValueError(f"{name} must be a GPU tensor")
+    if t.dim() == 2 and t.shape[0] > 1 and t.stride(1) == 1 and t.stride(0) >= t.shape[1] > 0:
+        return t.stride(0)
     if t.numel() == 0 or t.is_contiguous():
         return max(t.shape[-1], 1)
     if t.shape[-1] > 1 and t.stride(-1) != 1:
@@ -925,7 +951,7 @@ def ssd_add_norm_fwd(x, w, residual=None, scale=None, eps=1e-5, out=None, out_dt
     itself.  Returns (out, r)."""
     D, M = _rows_of(x, "x")
     shape = x.shape
-    xd = _dcode(x.dtype, "x")
+    xd = _code(x.dtype, "x")
     if residual is not None:
         if res_dtype not in (None, residual.dtype):
             raise TypeError(f"residual is {residual.dtype}, res_dtype {res_dtype}")
@@ -934,7 +960,7 @@ def ssd_add_norm_fwd(x, w, residual=None, scale=None, eps=1e-5, out=None, out_dt
         res_dtype = torch.float32 if residual_out is None else residual_out.dtype
     if out_dtype is None:
         out_dtype = x.dtype if out is None else out.dtype
-    rd, od = _dcode(res_dtype, "residual"), _dcode(out_dtype, "out")
+    rd, od = _code(res_dtype, "residual"), _code(out_dtype, "out")
     f32 = torch.float32
     px, ps, pr, pw, pro, po = _tensors(
         x, (x, "x", shape, x.dtype), (scale, "scale", (D,), f32),
@@ -948,7 +974,7 @@ def ssd_add_norm_fwd(x, w, residual=None, scale=None, eps=1e-5, out=None, out_dt
             residual_out = torch.empty(shape, dtype=res_dtype, device=x.device)
             pro = residual_out.data_ptr()
         _check(lib().ssd_add_norm_fwd(px, ps, pr, pw, eps, pro, po, M, D, xd, rd, od,
-                                      _stream(stream)))
+                                      _raw_stream(x)))
     return out, residual_out
 
 
@@ -963,7 +989,7 @@ def ssd_add_norm_bwd(dout, r, w, dres=None, scale=None, x=None, eps=1e-5, x_dtyp
     shape = r.shape
     if x_dtype is None:
         x_dtype = dout.dtype if x is None else x.dtype
-    xd, rd, od = _dcode(x_dtype, "x"), _dcode(r.dtype, "r"), _dcode(dout.dtype, "dout")
+    xd, rd, od = _code(x_dtype, "x"), _code(r.dtype, "r"), _code(dout.dtype, "dout")
     f32 = torch.float32
     pr, pd, pe, px, pw, ps = _tensors(
         r, (r, "r", shape, r.dtype), (dout, "dout", shape, dout.dtype),
@@ -978,7 +1004,7 @@ def ssd_add_norm_bwd(dout, r, w, dres=None, scale=None, x=None, eps=1e-5, x_dtyp
         _check(lib().ssd_add_norm_bwd(pd, pe, pr, px, ps, pw, eps, dresidual.data_ptr(),
                                       dx.data_ptr(), dw.data_ptr(),
                                       None if ds is None else ds.data_ptr(), M, D, xd, rd, od,
-                                      ws.data_ptr(), ws.numel(), _stream(stream)))
+                                      ws.data_ptr(), ws.numel(), _raw_stream(r)))
     return dict(dresidual=dresidual, dx=dx, dw=dw, dscale=ds)
 
 
@@ -993,7 +1019,7 @@ def ssd_gated_norm_fwd(y, z, w, groups=1, eps=1e-5, norm_before_gate=False, out=
     shape = y.shape
     if out_dtype is None:
         out_dtype = z.dtype if out is None else out.dtype
-    yd, zd, od = _dcode(y.dtype, "y"), _dcode(z.dtype, "z"), _dcode(out_dtype, "out")
+    yd, zd, od = _code(y.dtype, "y"), _code(z.dtype, "z"), _code(out_dtype, "out")
     _rows_like(z, "z", shape, z.dtype, y)
     py, pw, po = _tensors(y, (y, "y", shape, y.dtype), (w, "w", (D,), torch.float32),
                           (out, "out", shape, out_dtype))
@@ -1003,7 +1029,7 @@ def ssd_gated_norm_fwd(y, z, w, groups=1, eps=1e-5, norm_before_gate=False, out=
             out = torch.empty(shape, dtype=out_dtype, device=y.device)
             po = out.data_ptr()
         _check(lib().ssd_gated_norm_fwd(py, z.data_ptr(), ldz, pw, eps, int(bool(norm_before_gate)),
-                                        po, M, D, groups, yd, zd, od, _stream(stream)))
+                                        po, M, D, groups, yd, zd, od, _raw_stream(y)))
     return out
 
 
@@ -1015,7 +1041,7 @@ def ssd_gated_norm_bwd(dout, y, z, w, groups=1, eps=1e-5, norm_before_gate=False
     float32."""
     D, M = _rows_of(y, "y")
     shape = y.shape
-    yd, zd, od = _dcode(y.dtype, "y"), _dcode(z.dtype, "z"), _dcode(dout.dtype, "dout")
+    yd, zd, od = _code(y.dtype, "y"), _code(z.dtype, "z"), _code(dout.dtype, "dout")
     _rows_like(z, "z", shape, z.dtype, y)
     if dz is not None:
         _rows_like(dz, "dz", shape, z.dtype, y)
@@ -1031,7 +1057,7 @@ def ssd_gated_norm_bwd(dout, y, z, w, groups=1, eps=1e-5, norm_before_gate=False
         _check(lib().ssd_gated_norm_bwd(pd, py, z.data_ptr(), ldz, pw, eps,
                                         int(bool(norm_before_gate)), dy.data_ptr(), dz.data_ptr(),
                                         _lead(dz, "dz"), dw.data_ptr(), M, D, groups, yd, zd, od,
-                                        ws.data_ptr(), ws.numel(), _stream(stream)))
+                                        ws.data_ptr(), ws.numel(), _raw_stream(y)))
     return dict(dy=dy, dz=dz, dw=dw)
 
 
@@ -1052,7 +1078,7 @@ def ssd_conv1d_bwd(xbc, w, dx, dB, dC, bias=None, state_in=None, dstate_out=None
     HP, GN, K = dx.shape[2], dB.shape[2], w.shape[1]
     if Ch != HP + 2 * GN:
         raise ValueError(f"xbc has {Ch} channels, HP + 2*GN = {HP + 2 * GN}")
-    code = _dcode(xbc.dtype, "xbc")
+    code = _code(xbc.dtype, "xbc")
     f32 = torch.float32
     if dxbc is not None:
         _rows_like(dxbc, "dxbc", (Bsz, T, Ch), xbc.dtype, xbc)
@@ -1074,7 +1100,7 @@ def ssd_conv1d_bwd(xbc, w, dx, dB, dC, bias=None, state_in=None, dstate_out=None
                                     dxbc.data_ptr(), _lead(dxbc, "dxbc"), dw.data_ptr(),
                                     dbias.data_ptr(), None if dstate is None else dstate.data_ptr(),
                                     Bsz, T, HP, GN, K, code, ws.data_ptr(), ws.numel(),
-                                    _stream(stream)))
+                                    _raw_stream(xbc)))
     return dict(dxbc=dxbc, dw=dw, dbias=dbias, dstate_in=dstate)
 
 
@@ -1097,11 +1123,11 @@ def ssd_mixer_step(conv_state, h, arrivals, xbc, dt, w, A, bias=None, D=None, dt
     if Ch <= H * P or (Ch - H * P) % (2 * N):
         raise ValueError(f"xbc has {Ch} channels, not H*P + 2*G*N with H={H} P={P} N={N}")
     G, K = (Ch - H * P) // (2 * N), w.shape[1]
-    code = _dcode(xbc.dtype, "xbc")
+    code = _code(xbc.dtype, "xbc")
     f32 = torch.float32
     if y is not None:
         y_dtype = y.dtype
-    yd = _dcode(y_dtype, "y")
+    yd = _code(y_dtype, "y")
     _rows_like(xbc, "xbc", (Bsz, Ch), xbc.dtype, h)
     _rows_like(dt, "dt", (Bsz, H), xbc.dtype, h)
     ph, ps, pa, pm, pw, pA, pi, pD, pt, py = _tensors(
@@ -1116,5 +1142,5 @@ def ssd_mixer_step(conv_state, h, arrivals, xbc, dt, w, A, bias=None, D=None, dt
             py = y.data_ptr()
         _check(lib().ssd_mixer_step(ps, ph, pa, pm, nslots, xbc.data_ptr(), ldx, dt.data_ptr(), lddt,
                                     pw, pi, int(act), pA, pD, pt, dt_min, dt_max, py, yd, Bsz, H, P,
-                                    G, N, K, code, _stream(stream)))
+                                    G, N, K, code, _raw_stream(h)))
     return y

@@ -1022,7 +1022,9 @@ int ssd_conv1d_bwd(const void* xbc, long long ld, const float* w, const float* b
   SSD_TRY(check_conv_common(Bsz, HP, GN, lddx, K, act, V));
   if (T > (1 << 30)) return fail(SSD_EUNSUPPORTED, "T=%d above 2^30", T);
   const size_t Ch = static_cast<size_t>(HP) + 2 * static_cast<size_t>(GN);
-  if (Ch > (1u << 24)) return fail(SSD_EUNSUPPORTED, "%zu channels, at most 2^24", Ch);
+  // the rows of a run of tokens are addressed by 32-bit byte offsets
+  if (Ch > (1u << 24) || ld > (1 << 24) || lddx > (1 << 24))
+    return fail(SSD_EUNSUPPORTED, "%zu channels, ld=%lld, lddx=%lld: at most 2^24", Ch, ld, lddx);
   const bool has_tokens = T > 0;
   SSD_TRY(check_ptr(xbc, "xbc", 16, has_tokens));
   SSD_TRY(check_ptr(w, "w", 16, true));

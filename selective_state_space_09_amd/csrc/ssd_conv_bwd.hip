@@ -10,12 +10,23 @@
 // dstate_in.  v_t is recomputed from the inputs; nothing is saved by the
 // forward.
 //
-// The operation streams (x and dout in, dx out).  A lane owns 4 channels and
-// walks a run of tokens with the windows in_{t-3..t} and g_{t-3..t} and the
-// channel's five sums in registers, so a row is read once per run (plus 3
-// rows of halo on either side).  The four waves of a workgroup take runs of
-// the same channels and join their sums in LDS; each workgroup writes one row
-// of a partial-sum table that a second kernel adds up in a fixed order.
+// The operation streams (x and dout in, dx out).  A lane owns V channels and
+// walks a run of kRun tokens with the windows of inputs and gradients and the
+// channels' five sums in registers, so a row is read once per run (plus halo
+// rows that the cache serves).  To write din_p it needs g up to p + 3: it
+// starts with g_{t0..t0+2} and then, for each p, makes g_{p+3} and din_p.  The
+// sums take the tokens t = p + 3 (and 0..2 in a sequence's first run), so every
+// token is counted once without a mask.  Loads and stores are buffer accesses whose offsets are
+// pushed out of range where nothing may be touched, so no access sits in a
+// branch, and a block of kBlk tokens is loaded while the one before it is
+// computed.
+//
+// Workgroups own channels of one of the three outputs x, B, C (whose gradients
+// differ in type).  The four waves of a workgroup take runs of the same
+// channels and join their sums in LDS; each workgroup writes one row of a
+// partial-sum table that a second kernel adds up in a fixed order.
+
+#include <type_traits>
 
 #include "ssd_chunk_common.h"
 #include "ssd_internal.h"
@@ -25,32 +36,222 @@ namespace ssd {
 
 namespace {
 
-constexpr int kV = 4;        // channels per lane
-constexpr int kRun = 32;     // tokens per run
+// Measured at 2 x 2048 tokens of 4352 bf16 channels (both kernels): V = 2, runs
+// of 32, blocks of 8 30.9 us; blocks of 4 31.9; runs of 16 31.9, of 64 33.3
+// (fewer waves); V = 4 42.9 (half the waves at twice the registers).
+constexpr int kV = 2;      // channels per lane
+constexpr int kRun = 32;   // tokens per run
+constexpr int kBlk = 8;    // tokens loaded together
 constexpr int kMaxParts = 256;
+constexpr uint32_t kOOB = 0xFFFFFFF0u;
 
-template <typename T>
-__device__ __forceinline__ void load4(const T* p, float* f);
-template <>
-__device__ __forceinline__ void load4<float>(const float* p, float* f) {
-  const float4 q = *reinterpret_cast<const float4*>(p);
-  f[0] = q.x, f[1] = q.y, f[2] = q.z, f[3] = q.w;
-}
-template <>
-__device__ __forceinline__ void load4<uint16_t>(const uint16_t* p, float* f) {
-  const uint2 q = *reinterpret_cast<const uint2*>(p);
-  f[0] = __uint_as_float(q.x << 16), f[1] = __uint_as_float(q.x & 0xFFFF0000u);
-  f[2] = __uint_as_float(q.y << 16), f[3] = __uint_as_float(q.y & 0xFFFF0000u);
-}
-__device__ __forceinline__ void store4(float* p, const float* f) {
-  *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-}
-__device__ __forceinline__ void store4(uint16_t* p, const float* f) {
-  *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]));
+// V elements of type T at a byte offset of a buffer, as raw words
+template <typename T, int V>
+struct Raw {
+  static constexpr int BYTES = sizeof(T) * V, WORDS = BYTES / 4;
+  uint32_t w[WORDS];
+  __device__ __forceinline__ void load(buf_t b, uint32_t off) {
+    if constexpr (BYTES == 4) {
+      w[0] = __builtin_amdgcn_raw_buffer_load_b32(b, off, 0, 0);
+    } else if constexpr (BYTES == 8) {
+      const uint2 q = buf_load8(b, off);
+      w[0] = q.x, w[1] = q.y;
+    } else {
+      const uint4 q = buf_load16(b, off);
+      w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+    }
+  }
+  __device__ __forceinline__ float at(int v) const {
+    if constexpr (sizeof(T) == 4) return __uint_as_float(w[v]);
+    return __uint_as_float(v & 1 ? w[v >> 1] & 0xFFFF0000u : w[v >> 1] << 16);
+  }
+  __device__ __forceinline__ static void store(buf_t b, uint32_t off, const float* f) {
+    uint32_t w[WORDS];
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i)
+      w[i] = sizeof(T) == 4 ? __float_as_uint(f[i]) : pack_bf16x2(f[2 * i], f[2 * i + 1]);
+    if constexpr (BYTES == 4)
+      __builtin_amdgcn_raw_buffer_store_b32(w[0], b, off, 0, 0);
+    else if constexpr (BYTES == 8)
+      buf_store8(b, off, make_uint2(w[0], w[1]));
+    else
+      buf_store16(b, off, make_uint4(w[0], w[1], w[2], w[3]));
+  }
+};
+
+// One workgroup's share of a channel region of TD gradients: lane channels c
+// .. c+V-1 of the row (region channel cr of width W), runs `first`, first +
+// stride, ...
+template <typename T, typename TD, bool SILU>
+__device__ __forceinline__ void conv_bwd_body(
+    const T* __restrict__ xbc, long long ld, const float* __restrict__ w,
+    const float* __restrict__ bias, const float* __restrict__ state_in, const TD* __restrict__ dout,
+    const float* __restrict__ dstate_out, T* __restrict__ dxbc, long long lddx,
+    float* __restrict__ dstate_in, int Bsz, int Tn, int Ch, int c, int cr, int W, bool active,
+    long long first, long long stride, float (&dw)[kV][4], float (&db)[kV]) {
+  constexpr int V = kV;
+  const int nruns = Tn > 0 ? (Tn + kRun - 1) / kRun : 1;
+  const long long units = static_cast<long long>(Bsz) * nruns;
+  float wt[V][4], bs[V];
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const float4 q = *reinterpret_cast<const float4*>(w + static_cast<size_t>(active ? c + v : 0) * 4);
+    wt[v][0] = q.x, wt[v][1] = q.y, wt[v][2] = q.z, wt[v][3] = q.w;
+    bs[v] = bias && active ? bias[c + v] : 0.0f;
+  }
+  const uint32_t lim = 3u * static_cast<uint32_t>(Ch) * 4u;
+
+  for (long long u = first; u < units; u += stride) {
+    const int b = static_cast<int>(u / nruns);
+    const int t0 = static_cast<int>(u % nruns) * kRun;
+    const int base = t0 >= 3 ? t0 - 3 : 0;           // first row that the run reads
+    const int rows = min(Tn - base, kRun + 6);       // rows it may read
+    const size_t r0 = static_cast<size_t>(b) * Tn + base;
+    const buf_t xb = make_buf(xbc + r0 * ld, static_cast<uint32_t>(rows * ld * sizeof(T)));
+    const buf_t gb = make_buf(dout + r0 * W, static_cast<uint32_t>(static_cast<size_t>(rows) * W * sizeof(TD)));
+    const buf_t ob = make_buf(dxbc + r0 * lddx, static_cast<uint32_t>(rows * lddx * sizeof(T)));
+    const size_t so = static_cast<size_t>(b) * 3 * Ch;
+    const buf_t sb = make_buf(state_in + so, state_in ? lim : 0u);
+    const buf_t eb = make_buf(dstate_out + so, dstate_out ? lim : 0u);
+    auto off_x = [&](int p, long long pitch) -> uint32_t {  // row p of the sequence
+      return active && p >= 0 && p < Tn ? static_cast<uint32_t>(((p - base) * pitch + c) * sizeof(T)) : kOOB;
+    };
+    auto off_g = [&](int p) -> uint32_t {
+      return active && p < Tn ? static_cast<uint32_t>(((p - base) * static_cast<long long>(W) + cr) * sizeof(TD)) : kOOB;
+    };
+    auto off_s = [&](int row) -> uint32_t {  // row of a (3, Ch) state
+      return active && row >= 0 && row < 3 ? (static_cast<uint32_t>(row) * Ch + c) * 4u : kOOB;
+    };
+    Raw<T, V> px[6];
+    Raw<float, V> ps[3];
+    Raw<TD, V> pg[3];
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      px[j].load(xb, off_x(t0 - 3 + j, ld));
+      ps[j].load(sb, off_s(t0 + j));  // position t0 - 3 + j where that is negative
+    }
+#pragma unroll
+    for (int j = 0; j < 3; ++j) {
+      px[3 + j].load(xb, off_x(t0 + j, ld));
+      pg[j].load(gb, off_g(t0 + j));
+    }
+    Raw<T, V> nx[kBlk];
+    Raw<TD, V> ng[kBlk];
+#pragma unroll
+    for (int i = 0; i < kBlk; ++i) {
+      nx[i].load(xb, off_x(t0 + 3 + i, ld));
+      ng[i].load(gb, off_g(t0 + 3 + i));
+    }
+
+    float win[3][V], gw[3][V];  // inputs t-3 .. t-1, gradients t-3 .. t-1
+    // a state row is read only where the position is negative (t0 = 0), and
+    // there the input row reads as zero: one of the two is zero
+#pragma unroll
+    for (int j = 0; j < 3; ++j)
+#pragma unroll
+      for (int v = 0; v < V; ++v) win[j][v] = px[j].at(v) + (t0 == 0 ? ps[j].at(v) : 0.0f);
+
+    auto grad = [&](float x, float d, int v) -> float {
+      if constexpr (!SILU) return d;
+      float a = bs[v];
+#pragma unroll
+      for (int j = 0; j < 3; ++j) a = fmaf(wt[v][j], win[j][v], a);
+      a = fmaf(wt[v][3], x, a);
+      const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(a * -1.4426950408889634f));
+      return d * s * fmaf(a, 1.0f - s, 1.0f);
+    };
+    auto count = [&](float x, float g, int v) {
+      db[v] += g;
+#pragma unroll
+      for (int j = 0; j < 3; ++j) dw[v][j] = fmaf(g, win[j][v], dw[v][j]);
+      dw[v][3] = fmaf(g, x, dw[v][3]);
+    };
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        const float x = px[3 + i].at(v);
+        float g = 0.0f;
+        if (t0 + i < Tn) {
+          g = grad(x, pg[i].at(v), v);
+          if (t0 == 0) count(x, g, v);
+        }
+        gw[i][v] = g;
+        win[0][v] = win[1][v], win[1][v] = win[2][v], win[2][v] = x;
+      }
+    }
+    if (t0 == 0 && dstate_in) {  // positions -3, -2, -1: the carried state's gradient
+      const buf_t db_ = make_buf(dstate_in + so, lim);
+#pragma unroll
+      for (int j = 0; j < 3; ++j) {
+        Raw<float, V> e;
+        e.load(eb, off_s(j - Tn));  // dstate_out row p - (T - 3), p = j - 3
+        float o[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          o[v] = e.at(v);
+#pragma unroll
+          for (int i = 0; i <= j; ++i) o[v] = fmaf(wt[v][j - i], gw[i][v], o[v]);
+        }
+        Raw<float, V>::store(db_, off_s(j), o);
+      }
+    }
+    // the gradients of positions p0 .. p0 + kBlk - 1; at the sequence's end
+    // (EDGE) tokens past it count for nothing and dstate_out is added
+    auto block = [&](auto edge, int p0, const Raw<T, V>* cx, const Raw<TD, V>* cg) {
+#pragma unroll
+      for (int i = 0; i < kBlk; ++i) {
+        const int p = p0 + i;
+        float o[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float x = cx[i].at(v);
+          float g = 0.0f;
+          if (!edge.value || p + 3 < Tn) {
+            g = grad(x, cg[i].at(v), v);
+            count(x, g, v);
+          }
+          o[v] = fmaf(wt[v][3], gw[0][v], fmaf(wt[v][2], gw[1][v], fmaf(wt[v][1], gw[2][v], wt[v][0] * g)));
+          gw[0][v] = gw[1][v], gw[1][v] = gw[2][v], gw[2][v] = g;
+          win[0][v] = win[1][v], win[1][v] = win[2][v], win[2][v] = x;
+        }
+        if constexpr (edge.value) {
+          if (dstate_out && p >= Tn - 3) {
+            Raw<float, V> e;
+            e.load(eb, off_s(p - (Tn - 3)));
+#pragma unroll
+            for (int v = 0; v < V; ++v) o[v] += e.at(v);
+          }
+        }
+        Raw<T, V>::store(ob, off_x(p, lddx), o);
+      }
+    };
+#pragma unroll 1
+    for (int p0 = t0; p0 < min(t0 + kRun, Tn); p0 += kBlk) {
+      Raw<T, V> cx[kBlk];
+      Raw<TD, V> cg[kBlk];
+#pragma unroll
+      for (int i = 0; i < kBlk; ++i) cx[i] = nx[i], cg[i] = ng[i];
+      if (p0 + kBlk < t0 + kRun) {
+#pragma unroll
+        for (int i = 0; i < kBlk; ++i) {
+          nx[i].load(xb, off_x(p0 + kBlk + 3 + i, ld));
+          ng[i].load(gb, off_g(p0 + kBlk + 3 + i));
+        }
+      }
+      if (p0 + kBlk + 3 <= Tn)
+        block(std::false_type{}, p0, cx, cg);
+      else
+        block(std::true_type{}, p0, cx, cg);
+    }
+  }
 }
 
-// Grid: x = channel blocks of 64 lanes, y = workgroups over the (sequence,
-// run) units, four units at a time.
+// channel blocks of one output
+inline __host__ __device__ int region_blocks(int W) { return (W / kV + kWave - 1) / kWave; }
+
+// Grid: x = channel blocks of x, then B, then C; y = workgroups over the
+// (sequence, run) units, four at a time.
 template <typename T, bool SILU>
 __global__ __launch_bounds__(kThreads) void ssd_conv1d_bwd_kernel(
     const T* __restrict__ xbc, long long ld, const float* __restrict__ w,
@@ -59,104 +260,34 @@ __global__ __launch_bounds__(kThreads) void ssd_conv1d_bwd_kernel(
     const float* __restrict__ dstate_out, T* __restrict__ dxbc, long long lddx,
     float* __restrict__ dstate_in, float* __restrict__ part, int Bsz, int Tn, int HP, int GN) {
   const int Ch = HP + 2 * GN;
-  const int wid = wave_id();
-  const int c = (blockIdx.x * kWave + (threadIdx.x & (kWave - 1))) * kV;
-  const bool active = c < Ch;
-  const int nruns = Tn > 0 ? (Tn + kRun - 1) / kRun : 1;
-  const long long units = static_cast<long long>(Bsz) * nruns;
-  float wt[kV][4], bs[kV] = {}, dw[kV][4] = {}, db[kV] = {};
-#pragma unroll
-  for (int v = 0; v < kV; ++v) {
-    load4(w + static_cast<size_t>(active ? c + v : 0) * 4, wt[v]);
-  }
-  if (bias && active) load4(bias + c, bs);
-
-  for (long long u = static_cast<long long>(blockIdx.y) * 4 + wid; u < units;
-       u += static_cast<long long>(gridDim.y) * 4) {
-    if (!active) continue;
-    const int b = static_cast<int>(u / nruns);
-    const int t0 = static_cast<int>(u % nruns) * kRun;
-    const int t1 = min(t0 + kRun, Tn);
-    const size_t row0 = static_cast<size_t>(b) * Tn;
-    const float* st = state_in ? state_in + static_cast<size_t>(b) * 3 * Ch + c : nullptr;
-    auto in_at = [&](int p, float* f) {
-      if (p >= 0) {
-        load4(xbc + (row0 + p) * ld + c, f);
-      } else if (st) {
-        load4(st + static_cast<size_t>(3 + p) * Ch, f);
-      } else {
-        f[0] = f[1] = f[2] = f[3] = 0.0f;
-      }
-    };
-    auto dout_at = [&](int t, float* f) {
-      if (c < HP)
-        load4(dx + (row0 + t) * HP + c, f);
-      else if (c < HP + GN)
-        load4(dB + (row0 + t) * GN + (c - HP), f);
-      else
-        load4(dC + (row0 + t) * GN + (c - HP - GN), f);
-    };
-    float win[4][kV], gw[4][kV] = {};
-#pragma unroll
-    for (int j = 0; j < 3; ++j) in_at(t0 - 3 + j, win[j + 1]);
-    for (int t = t0; t < t1 + 3; ++t) {
-#pragma unroll
-      for (int j = 0; j < 3; ++j)
-#pragma unroll
-        for (int v = 0; v < kV; ++v) win[j][v] = win[j + 1][v], gw[j][v] = gw[j + 1][v];
-      if (t < Tn) {
-        float d[kV];
-        in_at(t, win[3]);
-        dout_at(t, d);
-#pragma unroll
-        for (int v = 0; v < kV; ++v) {
-          float g = d[v];
-          if (SILU) {
-            float a = bs[v];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) a = fmaf(wt[v][j], win[j][v], a);
-            const float s = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(a * -1.4426950408889634f));
-            g *= s * fmaf(a, 1.0f - s, 1.0f);
-          }
-          gw[3][v] = g;
-          if (t < t1) {
-            db[v] += g;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) dw[v][j] = fmaf(g, win[j][v], dw[v][j]);
-          }
-        }
-      } else {
-#pragma unroll
-        for (int v = 0; v < kV; ++v) gw[3][v] = 0.0f;
-      }
-      const int p = t - 3;
-      if (p < t0 && t0 > 0) continue;  // the run before writes those
-      float o[kV];
-#pragma unroll
-      for (int v = 0; v < kV; ++v)
-        o[v] = fmaf(wt[v][3], gw[0][v], fmaf(wt[v][2], gw[1][v], fmaf(wt[v][1], gw[2][v], wt[v][0] * gw[3][v])));
-      if (dstate_out && p >= Tn - 3) {
-        float e[kV];
-        load4(dstate_out + (static_cast<size_t>(b) * 3 + (p - (Tn - 3))) * Ch + c, e);
-#pragma unroll
-        for (int v = 0; v < kV; ++v) o[v] += e[v];
-      }
-      if (p >= 0)
-        store4(dxbc + (row0 + p) * lddx + c, o);
-      else if (dstate_in)
-        store4(dstate_in + (static_cast<size_t>(b) * 3 + (3 + p)) * Ch + c, o);
-    }
+  const int wid = wave_id(), lane = threadIdx.x & (kWave - 1);
+  const long long first = static_cast<long long>(blockIdx.y) * 4 + wid, stride = static_cast<long long>(gridDim.y) * 4;
+  const int nx = region_blocks(HP), ng = region_blocks(GN), bx = blockIdx.x;
+  float dw[kV][4] = {}, db[kV] = {};
+  int c;
+  bool active;
+  if (bx < nx) {
+    c = (bx * kWave + lane) * kV;
+    active = c < HP;
+    conv_bwd_body<T, T, SILU>(xbc, ld, w, bias, state_in, dx, dstate_out, dxbc, lddx, dstate_in, Bsz, Tn, Ch, c, c,
+                              HP, active, first, stride, dw, db);
+  } else {
+    const bool isC = bx >= nx + ng;
+    const int cr = ((bx - nx - (isC ? ng : 0)) * kWave + lane) * kV;
+    c = HP + (isC ? GN : 0) + cr;
+    active = cr < GN;
+    conv_bwd_body<T, float, SILU>(xbc, ld, w, bias, state_in, isC ? dC : dB, dstate_out, dxbc, lddx, dstate_in, Bsz,
+                                  Tn, Ch, c, cr, GN, active, first, stride, dw, db);
   }
 
-  // join the four waves: columns c*4 + j hold dw, 4 Ch + c dbias
-  __shared__ float buf[3][kWave][kV * 5];
-  const int lane = threadIdx.x & (kWave - 1);
+  // join the four waves: columns 4 c + j hold dw, 4 Ch + c dbias
+  __shared__ float buf[3][kV * 5][kWave];
   if (wid > 0) {
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) buf[wid - 1][lane][v * 4 + j] = dw[v][j];
-      buf[wid - 1][lane][16 + v] = db[v];
+      for (int j = 0; j < 4; ++j) buf[wid - 1][v * 5 + j][lane] = dw[v][j];
+      buf[wid - 1][v * 5 + 4][lane] = db[v];
     }
   }
   __syncthreads();
@@ -165,18 +296,20 @@ __global__ __launch_bounds__(kThreads) void ssd_conv1d_bwd_kernel(
 #pragma unroll
     for (int v = 0; v < kV; ++v) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) dw[v][j] += buf[0][lane][v * 4 + j] + buf[1][lane][v * 4 + j] + buf[2][lane][v * 4 + j];
-      db[v] += buf[0][lane][16 + v] + buf[1][lane][16 + v] + buf[2][lane][16 + v];
-      store4(p + static_cast<size_t>(c + v) * 4, dw[v]);
+      for (int k = 0; k < 3; ++k) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dw[v][j] += buf[k][v * 5 + j][lane];
+        db[v] += buf[k][v * 5 + 4][lane];
+      }
+      *reinterpret_cast<float4*>(p + static_cast<size_t>(c + v) * 4) = make_float4(dw[v][0], dw[v][1], dw[v][2], dw[v][3]);
+      p[4 * static_cast<size_t>(Ch) + c + v] = db[v];
     }
-    store4(p + 4 * static_cast<size_t>(Ch) + c, db);
   }
 }
 
 template <typename T>
 void launch_conv_bwd(const ConvBwdArgs& a, hipStream_t st) {
-  const int Ch = a.HP + 2 * a.GN;
-  const dim3 grid((Ch / kV + kWave - 1) / kWave, conv_bwd_parts(a.Bsz, a.T));
+  const dim3 grid(region_blocks(a.HP) + 2 * region_blocks(a.GN), conv_bwd_parts(a.Bsz, a.T));
   const T* xbc = static_cast<const T*>(a.xbc);
   const T* dx = static_cast<const T*>(a.dx);
   T* dxbc = static_cast<T*>(a.dxbc);

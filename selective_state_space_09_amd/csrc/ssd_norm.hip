@@ -314,21 +314,35 @@ __global__ __launch_bounds__(team_block<TPR>()) void ssd_gated_norm_bwd_kernel(
   write_part<TPR, K>(dw, buf, part + static_cast<size_t>(blockIdx.x) * D + c0, L);
 }
 
-// Grid: blocks of 64 columns; 4 waves split the parts.
-__global__ __launch_bounds__(kThreads) void ssd_sum_parts_kernel(const float* __restrict__ part,
-                                                                  int nparts, int n,
-                                                                  float* __restrict__ a, int na,
-                                                                  float* __restrict__ b) {
-  __shared__ float s[4][kWave];
-  const int lane = threadIdx.x & (kWave - 1), wv = threadIdx.x / kWave;
+// Grid: blocks of 64 columns; the 16 waves of a block split the parts, each
+// with eight loads in flight.
+constexpr int kSumWaves = 16;
+__global__ __launch_bounds__(kSumWaves* kWave) void ssd_sum_parts_kernel(
+    const float* __restrict__ part, int nparts, int n, float* __restrict__ a, int na,
+    float* __restrict__ b) {
+  constexpr int U = 8;
+  __shared__ float s[kSumWaves][kWave];
+  const int lane = threadIdx.x & (kWave - 1), wv = wave_id();
   const int col = blockIdx.x * kWave + lane;
   float acc = 0.0f;
-  if (col < n)
-    for (int p = wv; p < nparts; p += 4) acc += part[static_cast<size_t>(p) * n + col];
+  if (col < n) {
+    for (int p0 = wv; p0 < nparts; p0 += U * kSumWaves) {
+      float v[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int p = p0 + k * kSumWaves;  // past the table: the last row, not added
+        v[k] = part[static_cast<size_t>(p < nparts ? p : nparts - 1) * n + col];
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) acc += p0 + k * kSumWaves < nparts ? v[k] : 0.0f;
+    }
+  }
   s[wv][lane] = acc;
   __syncthreads();
   if (wv == 0 && col < n) {
-    const float t = (s[0][lane] + s[1][lane]) + (s[2][lane] + s[3][lane]);
+    float t = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kSumWaves; ++k) t += s[k][lane];
     if (col < na)
       a[col] = t;
     else
@@ -467,8 +481,8 @@ hipError_t gated_norm_bwd_t(const GatedNormArgs& a, hipStream_t st) {
 
 hipError_t sum_parts(const float* part, int nparts, int n, float* a, int na, float* b,
                      hipStream_t st) {
-  launch_k(true, ssd_sum_parts_kernel, dim3((n + kWave - 1) / kWave), dim3(kThreads), st, nullptr,
-           part, nparts, n, a, na, b);
+  launch_k(true, ssd_sum_parts_kernel, dim3((n + kWave - 1) / kWave), dim3(kSumWaves * kWave), st,
+           nullptr, part, nparts, n, a, na, b);
   return hipGetLastError();
 }
 
