@@ -656,7 +656,7 @@ int ssd_gated_norm_bwd(const void *dout, const void *y, const void *z,
  *   dstate_in  (Bsz, 3, Ch) float32, or NULL (not written)
  *   workspace  ssd_conv1d_bwd_workspace_size(...) bytes, 256-byte aligned
  * HP, GN, ld and lddx multiples of 8 (bf16) or 4 (fp32), pointers 16-byte
- * aligned, T <= 2^30, ld and lddx (and so Ch) <= 2^24.  T = 0: dstate_in is dstate_out, the sums
+ * aligned, T <= 2^30, Ch <= 2^24.  T = 0: dstate_in is dstate_out, the sums
  * are zero.  Sums in a fixed order (no atomics).  Outputs must not overlap
  * anything (such a call is rejected).
  */

@@ -1007,7 +1007,7 @@ size_t ssd_conv1d_bwd_workspace_size(int Bsz, int T, int HP, int GN) {
   if (Bsz <= 0 || T < 0 || HP <= 0 || GN < 0 || T > (1 << 30)) return 0;
   const size_t Ch = static_cast<size_t>(HP) + 2 * static_cast<size_t>(GN);
   if (Ch > (1u << 24)) return 0;
-  return round_ws(static_cast<size_t>(ssd::conv_bwd_parts(Bsz, T)) * 5 * Ch * 4);
+  return round_ws(static_cast<size_t>(ssd::conv_bwd_parts(Bsz, T, HP, GN)) * 5 * Ch * 4);
 }
 
 int ssd_conv1d_bwd(const void* xbc, long long ld, const float* w, const float* bias,
@@ -1022,9 +1022,7 @@ int ssd_conv1d_bwd(const void* xbc, long long ld, const float* w, const float* b
   SSD_TRY(check_conv_common(Bsz, HP, GN, lddx, K, act, V));
   if (T > (1 << 30)) return fail(SSD_EUNSUPPORTED, "T=%d above 2^30", T);
   const size_t Ch = static_cast<size_t>(HP) + 2 * static_cast<size_t>(GN);
-  // the rows of a run of tokens are addressed by 32-bit byte offsets
-  if (Ch > (1u << 24) || ld > (1 << 24) || lddx > (1 << 24))
-    return fail(SSD_EUNSUPPORTED, "%zu channels, ld=%lld, lddx=%lld: at most 2^24", Ch, ld, lddx);
+  if (Ch > (1u << 24)) return fail(SSD_EUNSUPPORTED, "%zu channels, at most 2^24", Ch);
   const bool has_tokens = T > 0;
   SSD_TRY(check_ptr(xbc, "xbc", 16, has_tokens));
   SSD_TRY(check_ptr(w, "w", 16, true));

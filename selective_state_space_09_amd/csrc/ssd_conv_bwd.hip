@@ -16,17 +16,17 @@
 // rows that the cache serves).  To write din_p it needs g up to p + 3: it
 // starts with g_{t0..t0+2} and then, for each p, makes g_{p+3} and din_p.  The
 // sums take the tokens t = p + 3 (and 0..2 in a sequence's first run), so every
-// token is counted once without a mask.  Loads and stores are buffer accesses whose offsets are
-// pushed out of range where nothing may be touched, so no access sits in a
-// branch, and a block of kBlk tokens is loaded while the one before it is
-// computed.
+// token is counted once without a mask.  Loads and stores are buffer accesses
+// with one descriptor per row, made in scalar registers: a row outside the
+// sequence has an empty one (loads give zero, stores are dropped), a lane
+// without channels an offset past every row.  So no access sits in a branch, a
+// lane's offset never changes, and a block of kBlk tokens is loaded while the
+// one before it is computed.
 //
 // Workgroups own channels of one of the three outputs x, B, C (whose gradients
 // differ in type).  The four waves of a workgroup take runs of the same
 // channels and join their sums in LDS; each workgroup writes one row of a
 // partial-sum table that a second kernel adds up in a fixed order.
-
-#include <type_traits>
 
 #include "ssd_chunk_common.h"
 #include "ssd_internal.h"
@@ -36,14 +36,17 @@ namespace ssd {
 
 namespace {
 
-// Measured at 2 x 2048 tokens of 4352 bf16 channels (both kernels): V = 2, runs
-// of 32, blocks of 8 30.9 us; blocks of 4 31.9; runs of 16 31.9, of 64 33.3
-// (fewer waves); V = 4 42.9 (half the waves at twice the registers).
-constexpr int kV = 2;      // channels per lane
-constexpr int kRun = 32;   // tokens per run
-constexpr int kBlk = 8;    // tokens loaded together
+// Measured at 2 x 2048 tokens of 4352 bf16 channels (both kernels; the whole
+// call's bytes as one elementwise library kernel: 21.7 us): V = 2, runs of 32,
+// blocks of 4 31.4 us, blocks of 8 34.3; with a second copy of the block's code
+// for its last tokens 33.4 (4) and 32.0 (8); one descriptor per run and the row
+// in the lane's offset 34.4 (8); V = 4 42.9 (half the waves).
+constexpr int kV = 2;       // channels per lane
+constexpr int kRunMax = 32;  // tokens per run, at most (a multiple of kBlk)
+constexpr int kBlk = 4;    // tokens loaded together
 constexpr int kMaxParts = 256;
-constexpr uint32_t kOOB = 0xFFFFFFF0u;
+// past every row and every (3, Ch) state, also with a state row's offset added
+constexpr uint32_t kOut = 0x60000000u;
 
 // V elements of type T at a byte offset of a buffer, as raw words
 template <typename T, int V>
@@ -88,9 +91,9 @@ __device__ __forceinline__ void conv_bwd_body(
     const float* __restrict__ bias, const float* __restrict__ state_in, const TD* __restrict__ dout,
     const float* __restrict__ dstate_out, T* __restrict__ dxbc, long long lddx,
     float* __restrict__ dstate_in, int Bsz, int Tn, int Ch, int c, int cr, int W, bool active,
-    long long first, long long stride, float (&dw)[kV][4], float (&db)[kV]) {
+    int run, long long first, long long stride, float (&dw)[kV][4], float (&db)[kV]) {
   constexpr int V = kV;
-  const int nruns = Tn > 0 ? (Tn + kRun - 1) / kRun : 1;
+  const int nruns = Tn > 0 ? (Tn + run - 1) / run : 1;
   const long long units = static_cast<long long>(Bsz) * nruns;
   float wt[V][4], bs[V];
 #pragma unroll
@@ -99,48 +102,61 @@ __device__ __forceinline__ void conv_bwd_body(
     wt[v][0] = q.x, wt[v][1] = q.y, wt[v][2] = q.z, wt[v][3] = q.w;
     bs[v] = bias && active ? bias[c + v] : 0.0f;
   }
-  const uint32_t lim = 3u * static_cast<uint32_t>(Ch) * 4u;
+  const uint32_t xlane = active ? static_cast<uint32_t>(c * sizeof(T)) : kOut;
+  const uint32_t glane = active ? static_cast<uint32_t>(cr * sizeof(TD)) : kOut;
+  const uint32_t slane = active ? static_cast<uint32_t>(c) * 4u : kOut;
+  const long long xpitch = ld * static_cast<long long>(sizeof(T)), opitch = lddx * static_cast<long long>(sizeof(T));
+  const long long gpitch = W * static_cast<long long>(sizeof(TD));
+  const uint32_t xbytes = static_cast<uint32_t>(Ch * sizeof(T)), gbytes = static_cast<uint32_t>(W * sizeof(TD));
+  const uint32_t sbytes = 3u * static_cast<uint32_t>(Ch) * 4u;
 
   for (long long u = first; u < units; u += stride) {
     const int b = static_cast<int>(u / nruns);
-    const int t0 = static_cast<int>(u % nruns) * kRun;
-    const int base = t0 >= 3 ? t0 - 3 : 0;           // first row that the run reads
-    const int rows = min(Tn - base, kRun + 6);       // rows it may read
-    const size_t r0 = static_cast<size_t>(b) * Tn + base;
-    const buf_t xb = make_buf(xbc + r0 * ld, static_cast<uint32_t>(rows * ld * sizeof(T)));
-    const buf_t gb = make_buf(dout + r0 * W, static_cast<uint32_t>(static_cast<size_t>(rows) * W * sizeof(TD)));
-    const buf_t ob = make_buf(dxbc + r0 * lddx, static_cast<uint32_t>(rows * lddx * sizeof(T)));
+    const int t0 = static_cast<int>(u % nruns) * run;
+    const long long r0 = static_cast<long long>(b) * Tn;
+    // rows are taken in order, each stream by a pointer that moves a row at a
+    // time: inputs from t0 - 3, gradients and results from t0
+    const char* xp = reinterpret_cast<const char*>(xbc) + (r0 + t0 - 3) * xpitch;
+    const char* gp = reinterpret_cast<const char*>(dout) + (r0 + t0) * gpitch;
+    char* op = reinterpret_cast<char*>(dxbc) + (r0 + t0) * opitch;
+    auto xrow = [&](int p) {
+      const buf_t r = make_buf(xp, p >= 0 && p < Tn ? xbytes : 0u);
+      xp += xpitch;
+      return r;
+    };
+    auto grow = [&](int p) {
+      const buf_t r = make_buf(gp, p < Tn ? gbytes : 0u);
+      gp += gpitch;
+      return r;
+    };
+    auto orow = [&](int p) {
+      const buf_t r = make_buf(op, p < Tn ? xbytes : 0u);
+      op += opitch;
+      return r;
+    };
     const size_t so = static_cast<size_t>(b) * 3 * Ch;
-    const buf_t sb = make_buf(state_in + so, state_in ? lim : 0u);
-    const buf_t eb = make_buf(dstate_out + so, dstate_out ? lim : 0u);
-    auto off_x = [&](int p, long long pitch) -> uint32_t {  // row p of the sequence
-      return active && p >= 0 && p < Tn ? static_cast<uint32_t>(((p - base) * pitch + c) * sizeof(T)) : kOOB;
-    };
-    auto off_g = [&](int p) -> uint32_t {
-      return active && p < Tn ? static_cast<uint32_t>(((p - base) * static_cast<long long>(W) + cr) * sizeof(TD)) : kOOB;
-    };
-    auto off_s = [&](int row) -> uint32_t {  // row of a (3, Ch) state
-      return active && row >= 0 && row < 3 ? (static_cast<uint32_t>(row) * Ch + c) * 4u : kOOB;
-    };
+    const buf_t sb = make_buf(state_in + so, state_in ? sbytes : 0u);
+    const buf_t eb = make_buf(dstate_out + so, dstate_out ? sbytes : 0u);
+    auto st = [&](int row) { return row >= 0 && row < 3 ? static_cast<uint32_t>(row) * Ch * 4u : kOut; };
     Raw<T, V> px[6];
     Raw<float, V> ps[3];
     Raw<TD, V> pg[3];
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
-      px[j].load(xb, off_x(t0 - 3 + j, ld));
-      ps[j].load(sb, off_s(t0 + j));  // position t0 - 3 + j where that is negative
+      px[j].load(xrow(t0 - 3 + j), xlane);
+      ps[j].load(sb, st(t0 + j) + slane);  // position t0 - 3 + j where that is negative
     }
 #pragma unroll
     for (int j = 0; j < 3; ++j) {
-      px[3 + j].load(xb, off_x(t0 + j, ld));
-      pg[j].load(gb, off_g(t0 + j));
+      px[3 + j].load(xrow(t0 + j), xlane);
+      pg[j].load(grow(t0 + j), glane);
     }
     Raw<T, V> nx[kBlk];
     Raw<TD, V> ng[kBlk];
 #pragma unroll
     for (int i = 0; i < kBlk; ++i) {
-      nx[i].load(xb, off_x(t0 + 3 + i, ld));
-      ng[i].load(gb, off_g(t0 + 3 + i));
+      nx[i].load(xrow(t0 + 3 + i), xlane);
+      ng[i].load(grow(t0 + 3 + i), glane);
     }
 
     float win[3][V], gw[3][V];  // inputs t-3 .. t-1, gradients t-3 .. t-1
@@ -171,21 +187,18 @@ __device__ __forceinline__ void conv_bwd_body(
 #pragma unroll
       for (int v = 0; v < V; ++v) {
         const float x = px[3 + i].at(v);
-        float g = 0.0f;
-        if (t0 + i < Tn) {
-          g = grad(x, pg[i].at(v), v);
-          if (t0 == 0) count(x, g, v);
-        }
+        const bool in = t0 + i < Tn;
+        const float g = in ? grad(x, pg[i].at(v), v) : 0.0f;
+        if (t0 == 0 && in) count(x, g, v);
         gw[i][v] = g;
         win[0][v] = win[1][v], win[1][v] = win[2][v], win[2][v] = x;
       }
     }
     if (t0 == 0 && dstate_in) {  // positions -3, -2, -1: the carried state's gradient
-      const buf_t db_ = make_buf(dstate_in + so, lim);
 #pragma unroll
       for (int j = 0; j < 3; ++j) {
         Raw<float, V> e;
-        e.load(eb, off_s(j - Tn));  // dstate_out row p - (T - 3), p = j - 3
+        e.load(eb, st(j - Tn) + slane);  // row p - (T - 3) of dstate_out, p = j - 3
         float o[V];
 #pragma unroll
         for (int v = 0; v < V; ++v) {
@@ -193,56 +206,44 @@ __device__ __forceinline__ void conv_bwd_body(
 #pragma unroll
           for (int i = 0; i <= j; ++i) o[v] = fmaf(wt[v][j - i], gw[i][v], o[v]);
         }
-        Raw<float, V>::store(db_, off_s(j), o);
+        Raw<float, V>::store(make_buf(dstate_in + so, sbytes), st(j) + slane, o);
       }
     }
-    // the gradients of positions p0 .. p0 + kBlk - 1; at the sequence's end
-    // (EDGE) tokens past it count for nothing and dstate_out is added
-    auto block = [&](auto edge, int p0, const Raw<T, V>* cx, const Raw<TD, V>* cg) {
-#pragma unroll
-      for (int i = 0; i < kBlk; ++i) {
-        const int p = p0 + i;
-        float o[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-          const float x = cx[i].at(v);
-          float g = 0.0f;
-          if (!edge.value || p + 3 < Tn) {
-            g = grad(x, cg[i].at(v), v);
-            count(x, g, v);
-          }
-          o[v] = fmaf(wt[v][3], gw[0][v], fmaf(wt[v][2], gw[1][v], fmaf(wt[v][1], gw[2][v], wt[v][0] * g)));
-          gw[0][v] = gw[1][v], gw[1][v] = gw[2][v], gw[2][v] = g;
-          win[0][v] = win[1][v], win[1][v] = win[2][v], win[2][v] = x;
-        }
-        if constexpr (edge.value) {
-          if (dstate_out && p >= Tn - 3) {
-            Raw<float, V> e;
-            e.load(eb, off_s(p - (Tn - 3)));
-#pragma unroll
-            for (int v = 0; v < V; ++v) o[v] += e.at(v);
-          }
-        }
-        Raw<T, V>::store(ob, off_x(p, lddx), o);
-      }
-    };
 #pragma unroll 1
-    for (int p0 = t0; p0 < min(t0 + kRun, Tn); p0 += kBlk) {
+    for (int p0 = t0; p0 < min(t0 + run, Tn); p0 += kBlk) {
       Raw<T, V> cx[kBlk];
       Raw<TD, V> cg[kBlk];
 #pragma unroll
       for (int i = 0; i < kBlk; ++i) cx[i] = nx[i], cg[i] = ng[i];
-      if (p0 + kBlk < t0 + kRun) {
+      if (p0 + kBlk < t0 + run) {
 #pragma unroll
         for (int i = 0; i < kBlk; ++i) {
-          nx[i].load(xb, off_x(p0 + kBlk + 3 + i, ld));
-          ng[i].load(gb, off_g(p0 + kBlk + 3 + i));
+          nx[i].load(xrow(p0 + kBlk + 3 + i), xlane);
+          ng[i].load(grow(p0 + kBlk + 3 + i), glane);
         }
       }
-      if (p0 + kBlk + 3 <= Tn)
-        block(std::false_type{}, p0, cx, cg);
-      else
-        block(std::true_type{}, p0, cx, cg);
+#pragma unroll
+      for (int i = 0; i < kBlk; ++i) {
+        const int p = p0 + i;
+        const bool end = p + 3 >= Tn;  // past the sequence: g = 0, nothing counted
+        float o[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+          const float x = cx[i].at(v);
+          const float g = end ? 0.0f : grad(x, cg[i].at(v), v);
+          if (!end) count(x, g, v);
+          o[v] = fmaf(wt[v][3], gw[0][v], fmaf(wt[v][2], gw[1][v], fmaf(wt[v][1], gw[2][v], wt[v][0] * g)));
+          gw[0][v] = gw[1][v], gw[1][v] = gw[2][v], gw[2][v] = g;
+          win[0][v] = win[1][v], win[1][v] = win[2][v], win[2][v] = x;
+        }
+        if (end && dstate_out) {
+          Raw<float, V> e;
+          e.load(eb, st(p - (Tn - 3)) + slane);
+#pragma unroll
+          for (int v = 0; v < V; ++v) o[v] += e.at(v);
+        }
+        Raw<T, V>::store(orow(p), xlane, o);
+      }
     }
   }
 }
@@ -258,7 +259,7 @@ __global__ __launch_bounds__(kThreads) void ssd_conv1d_bwd_kernel(
     const float* __restrict__ bias, const float* __restrict__ state_in, const T* __restrict__ dx,
     const float* __restrict__ dB, const float* __restrict__ dC,
     const float* __restrict__ dstate_out, T* __restrict__ dxbc, long long lddx,
-    float* __restrict__ dstate_in, float* __restrict__ part, int Bsz, int Tn, int HP, int GN) {
+    float* __restrict__ dstate_in, float* __restrict__ part, int Bsz, int Tn, int HP, int GN, int run) {
   const int Ch = HP + 2 * GN;
   const int wid = wave_id(), lane = threadIdx.x & (kWave - 1);
   const long long first = static_cast<long long>(blockIdx.y) * 4 + wid, stride = static_cast<long long>(gridDim.y) * 4;
@@ -270,14 +271,14 @@ __global__ __launch_bounds__(kThreads) void ssd_conv1d_bwd_kernel(
     c = (bx * kWave + lane) * kV;
     active = c < HP;
     conv_bwd_body<T, T, SILU>(xbc, ld, w, bias, state_in, dx, dstate_out, dxbc, lddx, dstate_in, Bsz, Tn, Ch, c, c,
-                              HP, active, first, stride, dw, db);
+                              HP, active, run, first, stride, dw, db);
   } else {
     const bool isC = bx >= nx + ng;
     const int cr = ((bx - nx - (isC ? ng : 0)) * kWave + lane) * kV;
     c = HP + (isC ? GN : 0) + cr;
     active = cr < GN;
     conv_bwd_body<T, float, SILU>(xbc, ld, w, bias, state_in, isC ? dC : dB, dstate_out, dxbc, lddx, dstate_in, Bsz,
-                                  Tn, Ch, c, cr, GN, active, first, stride, dw, db);
+                                  Tn, Ch, c, cr, GN, active, run, first, stride, dw, db);
   }
 
   // join the four waves: columns 4 c + j hold dw, 4 Ch + c dbias
@@ -307,9 +308,30 @@ __global__ __launch_bounds__(kThreads) void ssd_conv1d_bwd_kernel(
   }
 }
 
+// Run length and workgroups of a call: the longest run (least halo) that still
+// gives kMinWaves waves, four per SIMD.  Measured at 3 x 509 tokens of 1024 + 2 x
+// 1024 float32 channels with blocks of 8: runs of 32 (1152 waves) 19.4 us, of 16
+// 18.5, of 8 17.2.
+constexpr long long kMinWaves = 4096;
+constexpr int kRunMin = 8;
+struct Plan {
+  int run, blocks, parts;
+};
+Plan plan_of(int Bsz, int T, int HP, int GN) {
+  Plan p;
+  p.blocks = region_blocks(HP) + 2 * region_blocks(GN);
+  auto units = [&](int run) { return static_cast<long long>(Bsz) * (T > 0 ? (T + run - 1) / run : 1); };
+  p.run = kRunMax;
+  while (p.run > kRunMin && p.blocks * units(p.run) < kMinWaves) p.run /= 2;
+  const long long need = (units(p.run) + 3) / 4;
+  p.parts = static_cast<int>(need < kMaxParts ? need : kMaxParts);
+  return p;
+}
+
 template <typename T>
 void launch_conv_bwd(const ConvBwdArgs& a, hipStream_t st) {
-  const dim3 grid(region_blocks(a.HP) + 2 * region_blocks(a.GN), conv_bwd_parts(a.Bsz, a.T));
+  const Plan plan = plan_of(a.Bsz, a.T, a.HP, a.GN);
+  const dim3 grid(plan.blocks, plan.parts);
   const T* xbc = static_cast<const T*>(a.xbc);
   const T* dx = static_cast<const T*>(a.dx);
   T* dxbc = static_cast<T*>(a.dxbc);
@@ -317,21 +339,17 @@ void launch_conv_bwd(const ConvBwdArgs& a, hipStream_t st) {
   if (a.act)
     launch_k(true, ssd_conv1d_bwd_kernel<T, true>, grid, dim3(kThreads), st, nullptr, xbc, a.ld, a.w,
              a.bias, a.state_in, dx, a.dB, a.dC, a.dstate_out, dxbc, a.lddx, a.dstate_in, part, a.Bsz,
-             a.T, a.HP, a.GN);
+             a.T, a.HP, a.GN, plan.run);
   else
     launch_k(true, ssd_conv1d_bwd_kernel<T, false>, grid, dim3(kThreads), st, nullptr, xbc, a.ld, a.w,
              a.bias, a.state_in, dx, a.dB, a.dC, a.dstate_out, dxbc, a.lddx, a.dstate_in, part, a.Bsz,
-             a.T, a.HP, a.GN);
+             a.T, a.HP, a.GN, plan.run);
 }
 
 }  // namespace
 
-// rows of the partial-sum table: one per workgroup of four runs
-int conv_bwd_parts(int Bsz, int T) {
-  const long long units = static_cast<long long>(Bsz) * (T > 0 ? (T + kRun - 1) / kRun : 1);
-  const long long need = (units + 3) / 4;
-  return static_cast<int>(need < kMaxParts ? need : kMaxParts);
-}
+// rows of the partial-sum table
+int conv_bwd_parts(int Bsz, int T, int HP, int GN) { return plan_of(Bsz, T, HP, GN).parts; }
 
 hipError_t run_conv1d_bwd(const ConvBwdArgs& a, hipStream_t st) {
   if (a.dtype == 1)
@@ -341,7 +359,7 @@ hipError_t run_conv1d_bwd(const ConvBwdArgs& a, hipStream_t st) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int Ch = a.HP + 2 * a.GN;
-  return sum_parts(static_cast<const float*>(a.workspace), conv_bwd_parts(a.Bsz, a.T), 5 * Ch, a.dw,
+  return sum_parts(static_cast<const float*>(a.workspace), conv_bwd_parts(a.Bsz, a.T, a.HP, a.GN), 5 * Ch, a.dw,
                    4 * Ch, a.dbias, st);
 }
 

@@ -141,7 +141,7 @@ struct ConvBwdArgs {
   float* dbias;            // (Ch)
   float* dstate_in;        // (Bsz, 3, Ch) or NULL
   int Bsz, T, HP, GN, dtype;
-  void* workspace;         // conv_bwd_parts(Bsz, T) rows of 5 Ch floats
+  void* workspace;         // conv_bwd_parts(...) rows of 5 Ch floats
 };
 
 struct MixerStepArgs {
@@ -334,6 +334,6 @@ hipError_t run_mixer_step(const MixerStepArgs& a, hipStream_t st);
 // rows of the partial-sum tables of the backward passes
 int add_norm_parts(int M, int D);
 int gated_norm_parts(int M, int D, int groups);
-int conv_bwd_parts(int Bsz, int T);
+int conv_bwd_parts(int Bsz, int T, int HP, int GN);
 
 }  // namespace ssd

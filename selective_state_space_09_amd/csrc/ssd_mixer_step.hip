@@ -53,20 +53,65 @@ __global__ __launch_bounds__(kThreads) void ssd_mixer_step_kernel(
   constexpr int LPR = N / 4;            // lanes per state row
   constexpr int RPP = kThreads / LPR;   // rows covered by one pass of the block
   constexpr int UNR = 8;                // rows in flight per thread
+  constexpr int CI = 2;                 // convolved channels in flight per thread
   const int b = blockIdx.x / H, hh = blockIdx.x % H, g = hh / (H / G);
   const int tid = threadIdx.x;
-  const int HP = H * P, GN = G * N, Ch = HP + 2 * GN;
+  const int HP = H * P, GN = G * N, Ch = HP + 2 * GN, nch = P + 2 * N;
   const size_t yrow = static_cast<size_t>(blockIdx.x) * P;
 
-  // a row takes part if its slot exists and no earlier row has it
-  const int slot = slots ? slots[b] : b;
-  int skip = slot < 0 || slot >= nslots;
-  if (slots && !skip) {
-    int dup = 0;
-    for (int j = tid; j < b; j += kThreads) dup |= slots[j] == slot;
-    skip = __syncthreads_or(dup);
+  // a row takes part if its slot exists and no earlier row has it; until that
+  // is known it reads (only) slot 0's states
+  const int named = slots ? slots[b] : b;
+  const int slot = named >= 0 && named < nslots ? named : 0;
+  int skip = named != slot;
+  if (slots)
+    for (int j = tid; j < b; j += kThreads) skip |= slots[j] == named;
+
+  // loads in the order of their use: the convolution's, then the first pass of
+  // the state, which is in flight while the convolution is computed
+  float* cs = conv + static_cast<size_t>(slot) * 3 * Ch;
+  const T* row = xbc + static_cast<size_t>(b) * ldx;
+  auto channel = [&](int i) {
+    return i < P ? hh * P + i : i < P + N ? HP + g * N + (i - P) : HP + GN + g * N + (i - P - N);
+  };
+  float s0[CI], s1[CI], s2[CI], s3[CI], bs[CI];
+  float4 q[CI];
+#pragma unroll
+  for (int k = 0; k < CI; ++k) {
+    const int c = channel(min(tid + k * kThreads, nch - 1));
+    s0[k] = cs[c], s1[k] = cs[Ch + c], s2[k] = cs[2 * Ch + c], s3[k] = elem<T>(row[c]);
+    q[k] = *reinterpret_cast<const float4*>(w + static_cast<size_t>(c) * 4);
+    bs[k] = bias ? bias[c] : 0.0f;
   }
-  if (skip) {
+  const int col = tid % LPR, rsub = tid / LPR;
+  float* hrow = hpool + (static_cast<size_t>(slot) * H + hh) * P * N + col * 4;
+  f4v v[UNR];
+  auto load_rows = [&](int r0) {
+#pragma unroll
+    for (int k = 0; k < UNR; ++k) {
+      const int r = min(r0 + k * RPP, P - 1);
+      v[k] = __builtin_nontemporal_load(reinterpret_cast<const f4v*>(hrow + static_cast<size_t>(r) * N));
+    }
+  };
+  load_rows(rsub);
+
+  auto conv_value = [&](float a0, float a1, float a2, float a3, float4 t, float bb) {
+    float o = fmaf(t.w, a3, fmaf(t.z, a2, fmaf(t.y, a1, fmaf(t.x, a0, bb))));
+    if (act) o *= __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(o * -1.4426950408889634f));
+    return o;
+  };
+#pragma unroll
+  for (int k = 0; k < CI; ++k) {
+    const int i = tid + k * kThreads;
+    if (i < nch) lds[i] = conv_value(s0[k], s1[k], s2[k], s3[k], q[k], bs[k]);
+  }
+  for (int i = tid + CI * kThreads; i < nch; i += kThreads) {  // P + 2N > 512
+    const int c = channel(i);
+    lds[i] = conv_value(cs[c], cs[Ch + c], cs[2 * Ch + c], elem<T>(row[c]),
+                        *reinterpret_cast<const float4*>(w + static_cast<size_t>(c) * 4), bias ? bias[c] : 0.0f);
+  }
+  skip = __syncthreads_or(skip);
+  if (skip) {  // a padding row
     for (int p = tid; p < P; p += kThreads) {
       if (y_bf16)
         static_cast<uint16_t*>(y)[yrow + p] = 0;
@@ -75,44 +120,35 @@ __global__ __launch_bounds__(kThreads) void ssd_mixer_step_kernel(
     }
     return;
   }
-
-  float* cs = conv + static_cast<size_t>(slot) * 3 * Ch;
-  const T* row = xbc + static_cast<size_t>(b) * ldx;
-  const bool alone = H == G;  // no other workgroup reads this group's B and C
-  for (int i = tid; i < P + 2 * N; i += kThreads) {
-    const int c = i < P ? hh * P + i : i < P + N ? HP + g * N + (i - P) : HP + GN + g * N + (i - P - N);
-    const float s0 = cs[c], s1 = cs[Ch + c], s2 = cs[2 * Ch + c], s3 = elem<T>(row[c]);
-    const float4 q = *reinterpret_cast<const float4*>(w + static_cast<size_t>(c) * 4);
-    float v = bias ? bias[c] : 0.0f;
-    v = fmaf(q.x, s0, v);
-    v = fmaf(q.y, s1, v);
-    v = fmaf(q.z, s2, v);
-    v = fmaf(q.w, s3, v);
-    if (act) v *= __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(v * -1.4426950408889634f));
-    lds[i] = v;
-    if (i < P || alone) cs[c] = s1, cs[Ch + c] = s2, cs[2 * Ch + c] = s3;
-  }
-  __syncthreads();
-  // every conv value of this workgroup has arrived: count it in
+  // every conv value of this workgroup has arrived: count it in at the group's
+  // B and C, and move this head's own channels up
+  const bool alone = H == G;
   unsigned arrived = 0;
   if (!alone && tid == 0)
     arrived = atomicInc(arrivals + static_cast<size_t>(slot) * G + g, static_cast<unsigned>(H / G - 1));
+  const int own = alone ? nch : P;
+#pragma unroll
+  for (int k = 0; k < CI; ++k) {
+    const int i = tid + k * kThreads;
+    if (i < own) {
+      const int c = channel(i);
+      cs[c] = s1[k], cs[Ch + c] = s2[k], cs[2 * Ch + c] = s3[k];
+    }
+  }
+  for (int i = tid + CI * kThreads; i < own; i += kThreads) {
+    const int c = channel(i);
+    const float m1 = cs[Ch + c], m2 = cs[2 * Ch + c];
+    cs[c] = m1, cs[Ch + c] = m2, cs[2 * Ch + c] = elem<T>(row[c]);
+  }
 
   const float delta = step_size(elem<T>(dt[static_cast<size_t>(b) * lddt + hh]), dt_bias ? dt_bias[hh] : 0.0f, lo, hi);
   const float a = __expf(A[hh] * delta);
   const float Dh = D ? D[hh] : 0.0f;
-  const int col = tid % LPR, rsub = tid / LPR;
   float bq[4], cq[4];
 #pragma unroll
   for (int k = 0; k < 4; ++k) bq[k] = lds[P + col * 4 + k], cq[k] = lds[P + N + col * 4 + k];
-  float* hrow = hpool + (static_cast<size_t>(slot) * H + hh) * P * N + col * 4;
   for (int r0 = rsub; r0 < P; r0 += UNR * RPP) {
-    f4v v[UNR];
-#pragma unroll
-    for (int k = 0; k < UNR; ++k) {
-      const int r = r0 + k * RPP;
-      if (r < P) v[k] = __builtin_nontemporal_load(reinterpret_cast<const f4v*>(hrow + static_cast<size_t>(r) * N));
-    }
+    if (r0 != rsub) load_rows(r0);
 #pragma unroll
     for (int k = 0; k < UNR; ++k) {
       const int r = r0 + k * RPP;
@@ -146,9 +182,9 @@ __global__ __launch_bounds__(kThreads) void ssd_mixer_step_kernel(
   __syncthreads();
   if (!last) return;
   for (int i = tid; i < 2 * N; i += kThreads) {
-    const int c = i < N ? HP + g * N + i : HP + GN + g * N + (i - N);
-    const float s1 = cs[Ch + c], s2 = cs[2 * Ch + c];
-    cs[c] = s1, cs[Ch + c] = s2, cs[2 * Ch + c] = elem<T>(row[c]);
+    const int c = channel(P + i);
+    const float m1 = cs[Ch + c], m2 = cs[2 * Ch + c];
+    cs[c] = m1, cs[Ch + c] = m2, cs[2 * Ch + c] = elem<T>(row[c]);
   }
 }
 

@@ -38,7 +38,7 @@ __device__ __forceinline__ float fast_sigmoid(float v) {
 // alternating between calls, so that one barrier a call is enough).
 template <int TPR, int NV>
 __device__ __forceinline__ void team_sum(float (&v)[NV], float* red, int parity) {
-  constexpr int W = TPR < kWave ? TPR : kWave;
+  constexpr int W = TPR < kWave ? TPR : kWave;  // TPR > kWave: the team is the workgroup
 #pragma unroll
   for (int o = W / 2; o > 0; o >>= 1)
 #pragma unroll
@@ -60,112 +60,158 @@ __device__ __forceinline__ void team_sum(float (&v)[NV], float* red, int parity)
   }
 }
 
-template <int TPR>
-constexpr int team_block() {
-  return TPR > kThreads ? TPR : kThreads;
+// sum over the lane's own elements of f(i), i >= drop
+template <typename F>
+__device__ __forceinline__ void own_sum(float& acc, int drop, F f) {
+  if (drop == 0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc += f(i);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) acc += i >= drop ? f(i) : 0.0f;
+  }
 }
 
-template <int TPR, int K, typename TX, typename TR, typename TO>
-__global__ __launch_bounds__(team_block<TPR>()) void ssd_add_norm_kernel(
+// Threads of a workgroup: `several` shared by teams of up to a wave, which
+// need no barrier in their row loops; a wider team has a workgroup of its own.
+template <int TPR>
+constexpr int team_block(int several) {
+  return TPR > kWave ? TPR : several;
+}
+constexpr int kFwdThreads = 256, kBwdThreads = 512;
+
+template <int TPR, int K, bool SHORT, typename TX, typename TR, typename TO>
+__global__ __launch_bounds__(team_block<TPR>(kFwdThreads)) void ssd_add_norm_kernel(
     const TX* __restrict__ x, const float* __restrict__ scale, const TR* residual,
     const float* __restrict__ w, float eps, TR* r_out, TO* __restrict__ out, int M, int D) {
-  constexpr int BT = team_block<TPR>(), TEAMS = BT / TPR;
+  constexpr int BT = team_block<TPR>(kFwdThreads), TEAMS = BT / TPR;
   __shared__ float red[TPR > kWave ? 32 : 1];
   const int lane = threadIdx.x % TPR;
   const float inv = 1.0f / static_cast<float>(D);
+  Place pl[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) pl[k] = place_of<SHORT>(lane + k * TPR, D);
   int parity = 0;
   for (long long row = static_cast<long long>(blockIdx.x) * TEAMS + threadIdx.x / TPR; row < M;
        row += static_cast<long long>(gridDim.x) * TEAMS) {
     const size_t base = static_cast<size_t>(row) * D;
     float r[K][8];
+    Row8<float> wv[K];
+    {
+      Row8<TX> xv[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) xv[k] = row_load<SHORT>(x + base, pl[k], D);
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[k][i] = xv[k][i];
+    }
+    if (scale) {
+      Row8<float> sv[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) sv[k] = row_load<SHORT>(reload(scale), pl[k], D);
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[k][i] *= sv[k][i];
+    }
+    if (residual) {
+      Row8<TR> rv[K];
+#pragma unroll
+      for (int k = 0; k < K; ++k) rv[k] = row_load<SHORT>(residual + base, pl[k], D);
+#pragma unroll
+      for (int k = 0; k < K; ++k)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[k][i] += rv[k][i];
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) wv[k] = row_load<SHORT>(reload(w), pl[k], D);
     float ss[1] = {0.0f};
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int v = lane + k * TPR;
-      const Row8<TX> xv = row_load(x + base, v, D);
-      Row8<float> sv;
-      Row8<TR> rv;
-      rv.zero();
-      if (scale) sv = row_load(scale, v, D);
-      if (residual) rv = row_load(residual + base, v, D);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        r[k][i] = scale ? fmaf(sv[i], xv[i], rv[i]) : xv[i] + rv[i];
-        ss[0] = fmaf(r[k][i], r[k][i], ss[0]);
-      }
-    }
+    for (int k = 0; k < K; ++k) own_sum(ss[0], pl[k].drop, [&](int i) { return r[k][i] * r[k][i]; });
     team_sum<TPR, 1>(ss, red, parity);
     parity ^= 1;
     const float rstd = rsqrtf(ss[0] * inv + eps);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int v = lane + k * TPR;
-      const Row8<float> wv = row_load(w, v, D);
       float o[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = r[k][i] * rstd * wv[i];
-      if (r_out) row_store(r_out + base, v, D, r[k]);
-      row_store(out + base, v, D, o);
+      for (int i = 0; i < 8; ++i) o[i] = r[k][i] * rstd * wv[k][i];
+      if (r_out) row_store<SHORT>(r_out + base, pl[k], D, r[k]);
+      row_store<SHORT>(out + base, pl[k], D, o);
     }
   }
 }
 
 // The team's column sums (K vectors of 8 per lane) joined over the workgroup's
-// teams and written as columns col0 .. col0 + L - 1 of a partial row.
-template <int TPR, int K>
-__device__ __forceinline__ void write_part(const float (&acc)[K][8], float* buf, float* part, int L) {
-  constexpr int BT = team_block<TPR>(), TEAMS = BT / TPR;
-  const int lane = threadIdx.x % TPR;
+// teams and written as columns 0 .. L-1 of `part`.
+template <int TPR, int K, bool SHORT>
+__device__ __forceinline__ void write_part(const float (&acc)[K][8], const Place (&pl)[K], float* buf,
+                                           float* part, int L) {
+  constexpr int BT = team_block<TPR>(kBwdThreads), TEAMS = BT / TPR;
+  const int lane = threadIdx.x % TPR, team = threadIdx.x / TPR;
 #pragma unroll
   for (int k = 0; k < K; ++k) {
     if constexpr (TEAMS > 1) {
-      __syncthreads();
+      // buf[i][team][lane]: element i of the lane's vector; column j of the
+      // sums is element j / TPR of lane j % TPR
 #pragma unroll
-      for (int i = 0; i < 8; ++i) buf[threadIdx.x / TPR * (TPR * 8) + lane * 8 + i] = acc[k][i];
+      for (int i = 0; i < 8; ++i) buf[(i * TEAMS + team) * TPR + lane] = acc[k][i];
       __syncthreads();
-      for (int j = threadIdx.x; j < TPR * 8; j += BT) {
+      for (int j = threadIdx.x; j < TPR * 8; j += BT) {  // BT is a multiple of TPR: lane stays
+        const int i = j / TPR;
         float s = 0.0f;
-#pragma unroll
-        for (int t = 0; t < TEAMS; ++t) s += buf[t * (TPR * 8) + j];
-        const int col = k * TPR * 8 + j;
-        if (col < L) part[col] = s;
+#pragma unroll 8
+        for (int t = 0; t < TEAMS; ++t) s += buf[(i * TEAMS + t) * TPR + lane];
+        const Place p = place_of<SHORT>(lane + k * TPR, L);
+        if (i >= p.drop && i < (SHORT ? L : 8)) part[p.off + i] = s;
       }
+      __syncthreads();
     } else {
-      row_store(part, lane + k * TPR, L, acc[k]);
+      row_store<SHORT>(part, pl[k], L, acc[k]);
     }
   }
 }
 
-template <int TPR, int K, typename TX, typename TR, typename TO>
-__global__ __launch_bounds__(team_block<TPR>()) void ssd_add_norm_bwd_kernel(
+template <int TPR, int K, bool SHORT, typename TX, typename TR, typename TO>
+__global__ __launch_bounds__(team_block<TPR>(kBwdThreads)) void ssd_add_norm_bwd_kernel(
     const TO* __restrict__ dout, const TR* __restrict__ dres, const TR* __restrict__ r,
     const TX* __restrict__ x, const float* __restrict__ scale, const float* __restrict__ w,
     float eps, TR* __restrict__ dresidual, TX* __restrict__ dx, float* __restrict__ part, int M,
     int D, int want_dscale) {
-  constexpr int BT = team_block<TPR>(), TEAMS = BT / TPR;
+  constexpr int BT = team_block<TPR>(kBwdThreads), TEAMS = BT / TPR;
   __shared__ float red[TPR > kWave ? 64 : 1];
   __shared__ float buf[TEAMS > 1 ? BT * 8 : 1];
   const int lane = threadIdx.x % TPR;
   const float inv = 1.0f / static_cast<float>(D);
+  Place pl[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) pl[k] = place_of<SHORT>(lane + k * TPR, D);
   float dw[K][8] = {}, ds[K][8] = {};
   int parity = 0;
   for (long long row = static_cast<long long>(blockIdx.x) * TEAMS + threadIdx.x / TPR; row < M;
        row += static_cast<long long>(gridDim.x) * TEAMS) {
     const size_t base = static_cast<size_t>(row) * D;
-    Row8<TR> rv[K];
+    Row8<TR> rv[K], ev[K];
     Row8<TO> dv[K];
+    Row8<TX> xv[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) rv[k] = row_load<SHORT>(r + base, pl[k], D), dv[k] = row_load<SHORT>(dout + base, pl[k], D);
+    // what the second half needs arrives during the first (without dres or
+    // dscale the row itself is loaded again, from the cache, and not used)
+    const TR* second = dres ? dres : r;
+#pragma unroll
+    for (int k = 0; k < K; ++k) ev[k] = row_load<SHORT>(second + base, pl[k], D);
+    if (want_dscale) {
+#pragma unroll
+      for (int k = 0; k < K; ++k) xv[k] = row_load<SHORT>(x + base, pl[k], D);
+    }
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int v = lane + k * TPR;
-      rv[k] = row_load(r + base, v, D);
-      dv[k] = row_load(dout + base, v, D);
-      const Row8<float> wv = row_load(w, v, D);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        s[0] = fmaf(rv[k][i], rv[k][i], s[0]);
-        s[1] = fmaf(dv[k][i] * wv[i], rv[k][i], s[1]);
-      }
+      const Row8<float> wv = row_load<SHORT>(reload(w), pl[k], D);
+      own_sum(s[0], pl[k].drop, [&](int i) { return rv[k][i] * rv[k][i]; });
+      own_sum(s[1], pl[k].drop, [&](int i) { return dv[k][i] * wv[i] * rv[k][i]; });
     }
     team_sum<TPR, 2>(s, red, parity);
     parity ^= 1;
@@ -173,94 +219,103 @@ __global__ __launch_bounds__(team_block<TPR>()) void ssd_add_norm_bwd_kernel(
     const float m = s[1] * rstd * inv;  // mean(dn o n)
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int v = lane + k * TPR;
-      const Row8<float> wv = row_load(w, v, D);
-      Row8<TR> ev;
-      ev.zero();
-      if (dres) ev = row_load(dres + base, v, D);
+      remake(rv[k]);
+      remake(dv[k]);
+      const Row8<float> wv = row_load<SHORT>(reload(w), pl[k], D);
       float g[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float n = rv[k][i] * rstd;
         dw[k][i] = fmaf(dv[k][i], n, dw[k][i]);
-        g[i] = fmaf(rstd, fmaf(-n, m, dv[k][i] * wv[i]), ev[i]);
+        g[i] = rstd * fmaf(-n, m, dv[k][i] * wv[i]);
+        if (dres) g[i] += ev[k][i];
       }
-      if (dresidual) row_store(dresidual + base, v, D, g);
+      if (dresidual) row_store<SHORT>(dresidual + base, pl[k], D, g);
       if (want_dscale) {
-        const Row8<TX> xv = row_load(x + base, v, D);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ds[k][i] = fmaf(g[i], xv[i], ds[k][i]);
+        for (int i = 0; i < 8; ++i) ds[k][i] = fmaf(g[i], xv[k][i], ds[k][i]);
       }
       if (dx) {
         if (scale) {
-          const Row8<float> sv = row_load(scale, v, D);
+          const Row8<float> sv = row_load<SHORT>(reload(scale), pl[k], D);
 #pragma unroll
           for (int i = 0; i < 8; ++i) g[i] *= sv[i];
         }
-        row_store(dx + base, v, D, g);
+        row_store<SHORT>(dx + base, pl[k], D, g);
       }
     }
   }
   float* p = part + static_cast<size_t>(blockIdx.x) * (want_dscale ? 2 : 1) * D;
-  write_part<TPR, K>(dw, buf, p, D);
-  if (want_dscale) write_part<TPR, K>(ds, buf, p + D, D);
+  write_part<TPR, K, SHORT>(dw, pl, buf, p, D);
+  if (want_dscale) write_part<TPR, K, SHORT>(ds, pl, buf, p + D, D);
 }
 
 // Grid: x = row blocks, y = groups.
-template <int TPR, int K, typename TY, typename TZ, typename TO>
-__global__ __launch_bounds__(team_block<TPR>()) void ssd_gated_norm_kernel(
+template <int TPR, int K, bool SHORT, typename TY, typename TZ, typename TO>
+__global__ __launch_bounds__(team_block<TPR>(kFwdThreads)) void ssd_gated_norm_kernel(
     const TY* __restrict__ y, const TZ* __restrict__ z, long long ldz, const float* __restrict__ w,
     float eps, int before, TO* __restrict__ out, int M, int D, int L) {
-  constexpr int BT = team_block<TPR>(), TEAMS = BT / TPR;
+  constexpr int BT = team_block<TPR>(kFwdThreads), TEAMS = BT / TPR;
   __shared__ float red[TPR > kWave ? 32 : 1];
   const int lane = threadIdx.x % TPR;
   const float inv = 1.0f / static_cast<float>(L);
   const size_t c0 = static_cast<size_t>(blockIdx.y) * L;
+  Place pl[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) pl[k] = place_of<SHORT>(lane + k * TPR, L);
   int parity = 0;
   for (long long row = static_cast<long long>(blockIdx.x) * TEAMS + threadIdx.x / TPR; row < M;
        row += static_cast<long long>(gridDim.x) * TEAMS) {
     const size_t base = static_cast<size_t>(row) * D + c0;
+    Row8<TY> yv[K];
+    Row8<TZ> zv[K];
+    Row8<float> wv[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      yv[k] = row_load<SHORT>(y + base, pl[k], L);
+      zv[k] = row_load<SHORT>(z + static_cast<size_t>(row) * ldz + c0, pl[k], L);
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) wv[k] = row_load<SHORT>(reload(w) + c0, pl[k], L);
     float u[K][8], gt[K][8];
     float ss[1] = {0.0f};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int v = lane + k * TPR;
-      const Row8<TY> yv = row_load(y + base, v, L);
-      const Row8<TZ> zv = row_load(z + static_cast<size_t>(row) * ldz + c0, v, L);
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float s = zv[i] * fast_sigmoid(zv[i]);
-        u[k][i] = before ? yv[i] : yv[i] * s;
+        const float s = zv[k][i] * fast_sigmoid(zv[k][i]);
+        u[k][i] = before ? yv[k][i] : yv[k][i] * s;
         gt[k][i] = before ? s : 1.0f;
-        ss[0] = fmaf(u[k][i], u[k][i], ss[0]);
       }
+      own_sum(ss[0], pl[k].drop, [&](int i) { return u[k][i] * u[k][i]; });
     }
     team_sum<TPR, 1>(ss, red, parity);
     parity ^= 1;
     const float rstd = rsqrtf(ss[0] * inv + eps);
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int v = lane + k * TPR;
-      const Row8<float> wv = row_load(w + c0, v, L);
       float o[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) o[i] = u[k][i] * rstd * wv[i] * gt[k][i];
-      row_store(out + base, v, L, o);
+      for (int i = 0; i < 8; ++i) o[i] = u[k][i] * rstd * wv[k][i] * gt[k][i];
+      row_store<SHORT>(out + base, pl[k], L, o);
     }
   }
 }
 
-template <int TPR, int K, typename TY, typename TZ, typename TO>
-__global__ __launch_bounds__(team_block<TPR>()) void ssd_gated_norm_bwd_kernel(
+template <int TPR, int K, bool SHORT, typename TY, typename TZ, typename TO>
+__global__ __launch_bounds__(team_block<TPR>(kBwdThreads)) void ssd_gated_norm_bwd_kernel(
     const TO* __restrict__ dout, const TY* __restrict__ y, const TZ* __restrict__ z, long long ldz,
     const float* __restrict__ w, float eps, int before, TY* __restrict__ dy, TZ* __restrict__ dz,
     long long lddz, float* __restrict__ part, int M, int D, int L) {
-  constexpr int BT = team_block<TPR>(), TEAMS = BT / TPR;
+  constexpr int BT = team_block<TPR>(kBwdThreads), TEAMS = BT / TPR;
   __shared__ float red[TPR > kWave ? 64 : 1];
   __shared__ float buf[TEAMS > 1 ? BT * 8 : 1];
   const int lane = threadIdx.x % TPR;
   const float inv = 1.0f / static_cast<float>(L);
   const size_t c0 = static_cast<size_t>(blockIdx.y) * L;
+  Place pl[K];
+#pragma unroll
+  for (int k = 0; k < K; ++k) pl[k] = place_of<SHORT>(lane + k * TPR, L);
   float dw[K][8] = {};
   int parity = 0;
   for (long long row = static_cast<long long>(blockIdx.x) * TEAMS + threadIdx.x / TPR; row < M;
@@ -269,22 +324,25 @@ __global__ __launch_bounds__(team_block<TPR>()) void ssd_gated_norm_bwd_kernel(
     Row8<TY> yv[K];
     Row8<TZ> zv[K];
     Row8<TO> dv[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      yv[k] = row_load<SHORT>(y + base, pl[k], L);
+      zv[k] = row_load<SHORT>(z + static_cast<size_t>(row) * ldz + c0, pl[k], L);
+      dv[k] = row_load<SHORT>(dout + base, pl[k], L);
+    }
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int v = lane + k * TPR;
-      yv[k] = row_load(y + base, v, L);
-      zv[k] = row_load(z + static_cast<size_t>(row) * ldz + c0, v, L);
-      dv[k] = row_load(dout + base, v, L);
-      const Row8<float> wv = row_load(w + c0, v, L);
+      const Row8<float> wv = row_load<SHORT>(reload(w) + c0, pl[k], L);
+      float u[8], dn[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float gate = zv[k][i] * fast_sigmoid(zv[k][i]);
-        const float u = before ? yv[k][i] : yv[k][i] * gate;
-        const float dn = before ? dv[k][i] * gate : dv[k][i];
-        s[0] = fmaf(u, u, s[0]);
-        s[1] = fmaf(dn * wv[i], u, s[1]);
+        u[i] = before ? yv[k][i] : yv[k][i] * gate;
+        dn[i] = before ? dv[k][i] * gate : dv[k][i];
       }
+      own_sum(s[0], pl[k].drop, [&](int i) { return u[i] * u[i]; });
+      own_sum(s[1], pl[k].drop, [&](int i) { return dn[i] * wv[i] * u[i]; });
     }
     team_sum<TPR, 2>(s, red, parity);
     parity ^= 1;
@@ -292,8 +350,10 @@ __global__ __launch_bounds__(team_block<TPR>()) void ssd_gated_norm_bwd_kernel(
     const float m = s[1] * rstd * inv;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int v = lane + k * TPR;
-      const Row8<float> wv = row_load(w + c0, v, L);
+      remake(yv[k]);
+      remake(zv[k]);
+      remake(dv[k]);
+      const Row8<float> wv = row_load<SHORT>(reload(w) + c0, pl[k], L);
       float gy[8], gz[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -307,11 +367,11 @@ __global__ __launch_bounds__(team_block<TPR>()) void ssd_gated_norm_bwd_kernel(
         const float dg = before ? dv[k][i] * n * wv[i] : du * yv[k][i];
         gz[i] = dg * sig * fmaf(zz, 1.0f - sig, 1.0f);
       }
-      row_store(dy + base, v, L, gy);
-      row_store(dz + static_cast<size_t>(row) * lddz + c0, v, L, gz);
+      row_store<SHORT>(dy + base, pl[k], L, gy);
+      row_store<SHORT>(dz + static_cast<size_t>(row) * lddz + c0, pl[k], L, gz);
     }
   }
-  write_part<TPR, K>(dw, buf, part + static_cast<size_t>(blockIdx.x) * D + c0, L);
+  write_part<TPR, K, SHORT>(dw, pl, buf, part + static_cast<size_t>(blockIdx.x) * D + c0, L);
 }
 
 // Grid: blocks of 64 columns; the 16 waves of a block split the parts, each
@@ -350,7 +410,7 @@ __global__ __launch_bounds__(kSumWaves* kWave) void ssd_sum_parts_kernel(
   }
 }
 
-// rows a team covers at once, by the (TPR, K) that a segment of L elements gets
+// lanes of a team and vectors per lane for a row segment of L elements
 struct Shape {
   int tpr, k;
 };
@@ -358,109 +418,105 @@ Shape shape_of(int L) {
   if (L <= 128) return {16, 1};
   if (L <= 512) return {64, 1};
   if (L <= 1024) return {64, 2};
+  if (L <= 1536) return {64, 3};
   if (L <= 2048) return {64, 4};
   if (L <= 4096) return {256, 2};
+  if (L <= 6144) return {256, 3};
   if (L <= 8192) return {256, 4};
-  return {1024, 2};
+  return {512, 4};
 }
 
-int teams_of(int L) {
-  const int tpr = shape_of(L).tpr;
-  return tpr > kThreads ? 1 : kThreads / tpr;
-}
-
-// workgroups along the rows: enough for every row, at most `cap`
-int row_blocks(int M, int L, int groups, int cap) {
-  const int t = teams_of(L);
+// workgroups of `threads` along the rows: enough for every row, at most `cap`
+// over all groups
+int row_blocks(int M, int L, int groups, int threads, int cap) {
+  const int tpr = shape_of(L).tpr, t = tpr > kWave ? 1 : threads / tpr;
   const long long need = (static_cast<long long>(M) + t - 1) / t;
   const long long most = cap / groups > 0 ? cap / groups : 1;
   return static_cast<int>(need < most ? need : most);
 }
 
 constexpr int kFwdBlocks = 4096;
-constexpr int kBwdBlocks = 1024;
+#ifdef BWDB
+int bwd_blocks(int L) { return BWDB; }
+#else
+int bwd_blocks(int L) {
+  const Shape s = shape_of(L);
+  const int waves = s.tpr <= kWave && s.k <= 2 ? 4096 : 2048;
+  return waves * kWave / (s.tpr > kWave ? s.tpr : kBwdThreads);
+}
+#endif
 
-#define SSD_ROW_SHAPES(L, CASE)              \
-  switch (shape_of(L).tpr * 8 + shape_of(L).k) { \
-    CASE(16, 1)                              \
-    CASE(64, 1)                              \
-    CASE(64, 2)                              \
-    CASE(64, 4)                              \
-    CASE(256, 2)                             \
-    CASE(256, 4)                             \
-    CASE(1024, 2)                            \
-    default:                                 \
-      return hipErrorInvalidValue;           \
-  }
-
-template <typename TX, typename TR, typename TO>
-hipError_t add_norm_fwd_t(const AddNormArgs& a, hipStream_t st) {
-  const dim3 grid(row_blocks(a.M, a.D, 1, kFwdBlocks));
-#define SSD_CASE(TPR, K)                                                                          \
-  case TPR * 8 + K:                                                                               \
-    launch_k(true, ssd_add_norm_kernel<TPR, K, TX, TR, TO>, grid, dim3(team_block<TPR>()), st,     \
-             nullptr, static_cast<const TX*>(a.x), a.scale, static_cast<const TR*>(a.residual),  \
-             a.w, a.eps, static_cast<TR*>(a.r_out), static_cast<TO*>(a.out), a.M, a.D);           \
+// KERNEL<TPR, K, SHORT, types> for segments of L elements
+#define SSD_ROW_LAUNCH(KERNEL, L, grid, least, st, ...)                                              \
+  do {                                                                                               \
+    if (L < 8) {                                                                                     \
+      launch_k(true, KERNEL<16, 1, true, T0, T1, T2>, grid, dim3(team_block<16>(least)), st, nullptr, \
+               __VA_ARGS__);                                                                         \
+      break;                                                                                         \
+    }                                                                                                \
+    switch (shape_of(L).tpr * 8 + shape_of(L).k) {                                                   \
+      SSD_ROW_CASE(KERNEL, 16, 1, grid, least, st, __VA_ARGS__)                                      \
+      SSD_ROW_CASE(KERNEL, 64, 1, grid, least, st, __VA_ARGS__)                                      \
+      SSD_ROW_CASE(KERNEL, 64, 2, grid, least, st, __VA_ARGS__)                                      \
+      SSD_ROW_CASE(KERNEL, 64, 3, grid, least, st, __VA_ARGS__)                                      \
+      SSD_ROW_CASE(KERNEL, 64, 4, grid, least, st, __VA_ARGS__)                                      \
+      SSD_ROW_CASE(KERNEL, 256, 2, grid, least, st, __VA_ARGS__)                                     \
+      SSD_ROW_CASE(KERNEL, 256, 3, grid, least, st, __VA_ARGS__)                                     \
+      SSD_ROW_CASE(KERNEL, 256, 4, grid, least, st, __VA_ARGS__)                                     \
+      SSD_ROW_CASE(KERNEL, 512, 4, grid, least, st, __VA_ARGS__)                                     \
+    }                                                                                                \
+  } while (0)
+#define SSD_ROW_CASE(KERNEL, TPR, K, grid, least, st, ...)                                         \
+  case TPR * 8 + K:                                                                                \
+    launch_k(true, KERNEL<TPR, K, false, T0, T1, T2>, grid, dim3(team_block<TPR>(least)), st, nullptr, \
+             __VA_ARGS__);                                                                         \
     break;
-  SSD_ROW_SHAPES(a.D, SSD_CASE)
-#undef SSD_CASE
+
+template <typename T0, typename T1, typename T2>
+hipError_t add_norm_fwd_t(const AddNormArgs& a, hipStream_t st) {
+  const dim3 grid(row_blocks(a.M, a.D, 1, kFwdThreads, kFwdBlocks));
+  SSD_ROW_LAUNCH(ssd_add_norm_kernel, a.D, grid, kFwdThreads, st, static_cast<const T0*>(a.x), a.scale,
+                 static_cast<const T1*>(a.residual), a.w, a.eps, static_cast<T1*>(a.r_out),
+                 static_cast<T2*>(a.out), a.M, a.D);
   return hipGetLastError();
 }
 
-template <typename TX, typename TR, typename TO>
+template <typename T0, typename T1, typename T2>
 hipError_t add_norm_bwd_t(const AddNormArgs& a, hipStream_t st) {
-  const int nparts = row_blocks(a.M, a.D, 1, kBwdBlocks);
-  const dim3 grid(nparts);
+  const int nparts = add_norm_parts(a.M, a.D);
   float* part = static_cast<float*>(a.workspace);
-  if (nparts > 0)  // no rows: the sums are zero
-#define SSD_CASE(TPR, K)                                                                            \
-  case TPR * 8 + K:                                                                                 \
-    launch_k(true, ssd_add_norm_bwd_kernel<TPR, K, TX, TR, TO>, grid, dim3(team_block<TPR>()), st,   \
-             nullptr, static_cast<const TO*>(a.dout), static_cast<const TR*>(a.dres),               \
-             static_cast<const TR*>(a.r), static_cast<const TX*>(a.x), a.scale, a.w, a.eps,          \
-             static_cast<TR*>(a.dresidual), static_cast<TX*>(a.dx), part, a.M, a.D,                  \
-             static_cast<int>(a.dscale != nullptr));                                                 \
-    break;
-  SSD_ROW_SHAPES(a.D, SSD_CASE)
-#undef SSD_CASE
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (nparts > 0) {  // no rows: the sums are zero
+    SSD_ROW_LAUNCH(ssd_add_norm_bwd_kernel, a.D, dim3(nparts), kBwdThreads, st, static_cast<const T2*>(a.dout),
+                   static_cast<const T1*>(a.dres), static_cast<const T1*>(a.r), static_cast<const T0*>(a.x),
+                   a.scale, a.w, a.eps, static_cast<T1*>(a.dresidual), static_cast<T0*>(a.dx), part, a.M, a.D,
+                   static_cast<int>(a.dscale != nullptr));
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   return sum_parts(part, nparts, a.dscale ? 2 * a.D : a.D, a.dw, a.D, a.dscale, st);
 }
 
-template <typename TY, typename TZ, typename TO>
+template <typename T0, typename T1, typename T2>
 hipError_t gated_norm_fwd_t(const GatedNormArgs& a, hipStream_t st) {
   const int L = a.D / a.groups;
-  const dim3 grid(row_blocks(a.M, L, a.groups, kFwdBlocks), a.groups);
-#define SSD_CASE(TPR, K)                                                                          \
-  case TPR * 8 + K:                                                                               \
-    launch_k(true, ssd_gated_norm_kernel<TPR, K, TY, TZ, TO>, grid, dim3(team_block<TPR>()), st,   \
-             nullptr, static_cast<const TY*>(a.y), static_cast<const TZ*>(a.z), a.ldz, a.w,       \
-             a.eps, a.before, static_cast<TO*>(a.out), a.M, a.D, L);                               \
-    break;
-  SSD_ROW_SHAPES(L, SSD_CASE)
-#undef SSD_CASE
+  const dim3 grid(row_blocks(a.M, L, a.groups, kFwdThreads, kFwdBlocks), a.groups);
+  SSD_ROW_LAUNCH(ssd_gated_norm_kernel, L, grid, kFwdThreads, st, static_cast<const T0*>(a.y),
+                 static_cast<const T1*>(a.z), a.ldz, a.w, a.eps, a.before, static_cast<T2*>(a.out), a.M, a.D, L);
   return hipGetLastError();
 }
 
-template <typename TY, typename TZ, typename TO>
+template <typename T0, typename T1, typename T2>
 hipError_t gated_norm_bwd_t(const GatedNormArgs& a, hipStream_t st) {
   const int L = a.D / a.groups;
-  const int nparts = row_blocks(a.M, L, a.groups, kBwdBlocks);
-  const dim3 grid(nparts, a.groups);
+  const int nparts = gated_norm_parts(a.M, a.D, a.groups);
   float* part = static_cast<float*>(a.workspace);
-  if (nparts > 0)  // no rows: the sums are zero
-#define SSD_CASE(TPR, K)                                                                            \
-  case TPR * 8 + K:                                                                                 \
-    launch_k(true, ssd_gated_norm_bwd_kernel<TPR, K, TY, TZ, TO>, grid, dim3(team_block<TPR>()), st, \
-             nullptr, static_cast<const TO*>(a.dout), static_cast<const TY*>(a.y),                  \
-             static_cast<const TZ*>(a.z), a.ldz, a.w, a.eps, a.before, static_cast<TY*>(a.dy),       \
-             static_cast<TZ*>(a.dz), a.lddz, part, a.M, a.D, L);                                     \
-    break;
-  SSD_ROW_SHAPES(L, SSD_CASE)
-#undef SSD_CASE
-  const hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  if (nparts > 0) {
+    SSD_ROW_LAUNCH(ssd_gated_norm_bwd_kernel, L, dim3(nparts, a.groups), kBwdThreads, st,
+                   static_cast<const T2*>(a.dout), static_cast<const T0*>(a.y), static_cast<const T1*>(a.z), a.ldz,
+                   a.w, a.eps, a.before, static_cast<T0*>(a.dy), static_cast<T1*>(a.dz), a.lddz, part, a.M, a.D, L);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   return sum_parts(part, nparts, a.D, a.dw, a.D, nullptr, st);
 }
 
@@ -486,9 +542,9 @@ hipError_t sum_parts(const float* part, int nparts, int n, float* a, int na, flo
   return hipGetLastError();
 }
 
-int add_norm_parts(int M, int D) { return row_blocks(M, D, 1, kBwdBlocks); }
+int add_norm_parts(int M, int D) { return row_blocks(M, D, 1, kBwdThreads, bwd_blocks(D)); }
 int gated_norm_parts(int M, int D, int groups) {
-  return row_blocks(M, D / groups, groups, kBwdBlocks);
+  return row_blocks(M, D / groups, groups, kBwdThreads, bwd_blocks(D / groups));
 }
 
 hipError_t run_add_norm(const AddNormArgs& a, hipStream_t st) {

@@ -11,11 +11,12 @@
 namespace ssd {
 
 // 16 bytes at an address that is only element-aligned.  gfx950 takes
-// unaligned global vector accesses, so a row of odd length needs no scalar
-// path except for its last, partial vector.
+// unaligned global vector accesses, so rows of odd length or stride need no
+// scalar path.
 typedef uint32_t u32x4_e2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t u32x4_e4 __attribute__((ext_vector_type(4), aligned(4)));
 
+// eight consecutive elements of a row
 template <typename T>
 struct Row8;
 
@@ -26,14 +27,13 @@ struct Row8<float> {
     a = *reinterpret_cast<const u32x4_e4*>(p);
     b = *reinterpret_cast<const u32x4_e4*>(p + 4);
   }
-  // elements at and past n read as zero
-  __device__ __forceinline__ void load_tail(const float* p, int n) {
+  // the n < 8 elements of a row shorter than a vector; zeros behind them
+  __device__ __forceinline__ void load_short(const float* p, int n) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) a[i] = i < n ? __float_as_uint(p[i]) : 0u;
 #pragma unroll
     for (int i = 0; i < 4; ++i) b[i] = 4 + i < n ? __float_as_uint(p[4 + i]) : 0u;
   }
-  __device__ __forceinline__ void zero() { a = 0u, b = 0u; }
   __device__ __forceinline__ float operator[](int i) const {
     return __uint_as_float(i < 4 ? a[i] : b[i - 4]);
   }
@@ -51,14 +51,13 @@ template <>
 struct Row8<uint16_t> {
   u32x4_e2 a;
   __device__ __forceinline__ void load(const uint16_t* p) { a = *reinterpret_cast<const u32x4_e2*>(p); }
-  __device__ __forceinline__ void load_tail(const uint16_t* p, int n) {
+  __device__ __forceinline__ void load_short(const uint16_t* p, int n) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t lo = 2 * i < n ? p[2 * i] : 0u, hi = 2 * i + 1 < n ? p[2 * i + 1] : 0u;
       a[i] = lo | hi << 16;
     }
   }
-  __device__ __forceinline__ void zero() { a = 0u; }
   __device__ __forceinline__ float operator[](int i) const {
     return __uint_as_float(i & 1 ? a[i >> 1] & 0xFFFF0000u : a[i >> 1] << 16);
   }
@@ -73,28 +72,65 @@ struct Row8<uint16_t> {
   }
 };
 
-// vector v (elements 8v .. 8v+7) of a row of L elements
+// Hides where a value comes from: the compiler neither keeps what it loaded
+// through p (a weight row, the same for every row of a loop) nor what it made
+// of r in registers from one use to the next, which would cost the waves that
+// hide the latency of the rows.
 template <typename T>
-__device__ __forceinline__ Row8<T> row_load(const T* row, int v, int L) {
+__device__ __forceinline__ const T* reload(const T* p) {
+  asm volatile("" : "+s"(p));
+  return p;
+}
+__device__ __forceinline__ void remake(Row8<float>& r) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t a = r.a[i], b = r.b[i];
+    asm volatile("" : "+v"(a), "+v"(b));
+    r.a[i] = a, r.b[i] = b;
+  }
+}
+__device__ __forceinline__ void remake(Row8<uint16_t>& r) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t a = r.a[i];
+    asm volatile("" : "+v"(a));
+    r.a[i] = a;
+  }
+}
+
+// A lane's place for vector v of a row of L elements.  Every lane loads eight
+// elements without a branch: the row's last, partial vector is read as the
+// row's last eight elements, of which the first `drop` belong to the vector
+// before; a vector past the row reads the same and drops them all.  Elements
+// i < drop are left out of sums and stores.  SHORT: L < 8, one vector.
+struct Place {
+  int off, drop;
+};
+template <bool SHORT>
+__device__ __forceinline__ Place place_of(int v, int L) {
+  Place p;
+  p.off = SHORT ? 0 : min(8 * v, L - 8);
+  p.drop = SHORT ? (v == 0 ? 0 : 8) : min(8 * v - p.off, 8);
+  return p;
+}
+template <bool SHORT, typename T>
+__device__ __forceinline__ Row8<T> row_load(const T* row, Place pl, int L) {
   Row8<T> r;
-  const int n = L - 8 * v;
-  if (n >= 8)
-    r.load(row + 8 * v);
-  else if (n > 0)
-    r.load_tail(row + 8 * v, n);
+  if constexpr (SHORT)
+    r.load_short(row, L);
   else
-    r.zero();
+    r.load(row + pl.off);
   return r;
 }
-template <typename T>
-__device__ __forceinline__ void row_store(T* row, int v, int L, const float* f) {
-  const int n = L - 8 * v;
-  if (n >= 8) {
-    Row8<T>::store(row + 8 * v, f);
+template <bool SHORT, typename T>
+__device__ __forceinline__ void row_store(T* row, Place pl, int L, const float* f) {
+  if (!SHORT && pl.drop == 0) {
+    Row8<T>::store(row + pl.off, f);
   } else {
+    const int n = SHORT ? L : 8;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-      if (i < n) Row8<T>::store1(row + 8 * v + i, f[i]);
+      if (i >= pl.drop && i < n) Row8<T>::store1(row + pl.off + i, f[i]);
   }
 }
 
