@@ -410,72 +410,93 @@ __global__ __launch_bounds__(kSumWaves* kWave) void ssd_sum_parts_kernel(
   }
 }
 
-// lanes of a team and vectors per lane for a row segment of L elements
+// Lanes of a team and vectors per lane for a row segment of L elements.
 struct Shape {
   int tpr, k;
 };
-Shape shape_of(int L) {
+// Forward: one vector per lane up to 8192 elements.  The few instructions per
+// wave set the time of a small batch (one row of 2048: 256 lanes 2.7 us, 64
+// lanes of four vectors 3.4), and large batches stream either way (4096 x 2048:
+// 17.1 and 16.9 us; 512 x 16384: 19.7 and, with 512 lanes of four, 17.5).
+Shape fwd_shape(int L) {
   if (L <= 128) return {16, 1};
   if (L <= 512) return {64, 1};
   if (L <= 1024) return {64, 2};
-  if (L <= 1536) return {64, 3};
-  if (L <= 2048) return {64, 4};
-  if (L <= 4096) return {256, 2};
-  if (L <= 6144) return {256, 3};
-  if (L <= 8192) return {256, 4};
+  if (L <= 2048) return {256, 1};
+  if (L <= 4096) return {512, 1};
+  if (L <= 8192) return {1024, 1};
+  return {1024, 2};
+}
+// Backward: each lane also holds the column sums of its vectors.  Measured for
+// the residual norm (bf16 x and dout, float32 r and dres, 2^23 elements) and,
+// after the slash, the gated one (bf16, 2^24): L = 2048 with 256 lanes of one
+// vector 37.5 / 44.5 us, 64 of four 38.9 / 47.6; 4096 with 512 of one 37.6 /
+// 46.4, 256 of two 41.0 / 49.5; 8192 with 512 of two 45.4 / 45.8, 256 of four
+// 44.4 / 52.6, 1024 of one 44.3 / 49.1; 16384 with 512 of four 46.7, 1024 of
+// two 55.9.
+Shape bwd_shape(int L) {
+  if (L <= 128) return {16, 1};
+  if (L <= 512) return {64, 1};
+  if (L <= 1024) return {64, 2};
+  if (L <= 2048) return {256, 1};
+  if (L <= 4096) return {512, 1};
+  if (L <= 8192) return {512, 2};
   return {512, 4};
 }
 
-// workgroups of `threads` along the rows: enough for every row, at most `cap`
-// over all groups
-int row_blocks(int M, int L, int groups, int threads, int cap) {
-  const int tpr = shape_of(L).tpr, t = tpr > kWave ? 1 : threads / tpr;
+// workgroups of `several` threads (or one team) along the rows: enough for
+// every row, at most `cap` over all groups
+int row_blocks(int M, Shape s, int groups, int several, int cap) {
+  const int t = s.tpr > kWave ? 1 : several / s.tpr;
   const long long need = (static_cast<long long>(M) + t - 1) / t;
   const long long most = cap / groups > 0 ? cap / groups : 1;
   return static_cast<int>(need < most ? need : most);
 }
-
 constexpr int kFwdBlocks = 4096;
-#ifdef BWDB
-int bwd_blocks(int L) { return BWDB; }
-#else
-int bwd_blocks(int L) {
-  const Shape s = shape_of(L);
-  const int waves = s.tpr <= kWave && s.k <= 2 ? 4096 : 2048;
-  return waves * kWave / (s.tpr > kWave ? s.tpr : kBwdThreads);
+// Backward: every workgroup writes a row of `sums` vectors of partial sums, so
+// few are wanted, but their waves have to keep the memory busy: 512, except
+// 1024 where teams of four waves write one sum (4096 x 2 norms of 2048: 44.2
+// us, at 512 47.9; the residual norm's two sums there: 38.7 and 37.5), and 256
+// of the widest (512 x 16384: 46.7 us, at 512 58.8).
+int bwd_blocks(int L, int sums) {
+  const Shape s = bwd_shape(L);
+  return s.tpr == 256 && sums == 1 ? 1024 : s.k == 4 ? 256 : 512;
 }
-#endif
 
 // KERNEL<TPR, K, SHORT, types> for segments of L elements
-#define SSD_ROW_LAUNCH(KERNEL, L, grid, least, st, ...)                                              \
-  do {                                                                                               \
-    if (L < 8) {                                                                                     \
-      launch_k(true, KERNEL<16, 1, true, T0, T1, T2>, grid, dim3(team_block<16>(least)), st, nullptr, \
-               __VA_ARGS__);                                                                         \
-      break;                                                                                         \
-    }                                                                                                \
-    switch (shape_of(L).tpr * 8 + shape_of(L).k) {                                                   \
-      SSD_ROW_CASE(KERNEL, 16, 1, grid, least, st, __VA_ARGS__)                                      \
-      SSD_ROW_CASE(KERNEL, 64, 1, grid, least, st, __VA_ARGS__)                                      \
-      SSD_ROW_CASE(KERNEL, 64, 2, grid, least, st, __VA_ARGS__)                                      \
-      SSD_ROW_CASE(KERNEL, 64, 3, grid, least, st, __VA_ARGS__)                                      \
-      SSD_ROW_CASE(KERNEL, 64, 4, grid, least, st, __VA_ARGS__)                                      \
-      SSD_ROW_CASE(KERNEL, 256, 2, grid, least, st, __VA_ARGS__)                                     \
-      SSD_ROW_CASE(KERNEL, 256, 3, grid, least, st, __VA_ARGS__)                                     \
-      SSD_ROW_CASE(KERNEL, 256, 4, grid, least, st, __VA_ARGS__)                                     \
-      SSD_ROW_CASE(KERNEL, 512, 4, grid, least, st, __VA_ARGS__)                                     \
-    }                                                                                                \
-  } while (0)
-#define SSD_ROW_CASE(KERNEL, TPR, K, grid, least, st, ...)                                         \
-  case TPR * 8 + K:                                                                                \
-    launch_k(true, KERNEL<TPR, K, false, T0, T1, T2>, grid, dim3(team_block<TPR>(least)), st, nullptr, \
-             __VA_ARGS__);                                                                         \
+#define SSD_ROW_CASE(KERNEL, TPR, K, grid, several, st, ...)                                   \
+  case TPR * 8 + K:                                                                            \
+    launch_k(true, KERNEL<TPR, K, false, T0, T1, T2>, grid, dim3(team_block<TPR>(several)), st, \
+             nullptr, __VA_ARGS__);                                                            \
     break;
+#define SSD_ROW_LAUNCH(KERNEL, L, shape, WIDE, grid, several, st, ...)                            \
+  do {                                                                                            \
+    if (L < 8) {                                                                                  \
+      launch_k(true, KERNEL<16, 1, true, T0, T1, T2>, grid, dim3(team_block<16>(several)), st,     \
+               nullptr, __VA_ARGS__);                                                             \
+      break;                                                                                      \
+    }                                                                                             \
+    switch (shape.tpr * 8 + shape.k) {                                                            \
+      SSD_ROW_CASE(KERNEL, 16, 1, grid, several, st, __VA_ARGS__)                                 \
+      SSD_ROW_CASE(KERNEL, 64, 1, grid, several, st, __VA_ARGS__)                                 \
+      SSD_ROW_CASE(KERNEL, 64, 2, grid, several, st, __VA_ARGS__)                                 \
+      SSD_ROW_CASE(KERNEL, 256, 1, grid, several, st, __VA_ARGS__)                                \
+      SSD_ROW_CASE(KERNEL, 512, 1, grid, several, st, __VA_ARGS__)                                \
+      WIDE(KERNEL, grid, several, st, __VA_ARGS__)                                                \
+    }                                                                                             \
+  } while (0)
+#define SSD_FWD_WIDE(KERNEL, grid, several, st, ...)               \
+  SSD_ROW_CASE(KERNEL, 1024, 1, grid, several, st, __VA_ARGS__)    \
+  SSD_ROW_CASE(KERNEL, 1024, 2, grid, several, st, __VA_ARGS__)
+#define SSD_BWD_WIDE(KERNEL, grid, several, st, ...)               \
+  SSD_ROW_CASE(KERNEL, 512, 2, grid, several, st, __VA_ARGS__)     \
+  SSD_ROW_CASE(KERNEL, 512, 4, grid, several, st, __VA_ARGS__)
 
 template <typename T0, typename T1, typename T2>
 hipError_t add_norm_fwd_t(const AddNormArgs& a, hipStream_t st) {
-  const dim3 grid(row_blocks(a.M, a.D, 1, kFwdThreads, kFwdBlocks));
-  SSD_ROW_LAUNCH(ssd_add_norm_kernel, a.D, grid, kFwdThreads, st, static_cast<const T0*>(a.x), a.scale,
+  const Shape shape = fwd_shape(a.D);
+  const dim3 grid(row_blocks(a.M, shape, 1, kFwdThreads, kFwdBlocks));
+  SSD_ROW_LAUNCH(ssd_add_norm_kernel, a.D, shape, SSD_FWD_WIDE, grid, kFwdThreads, st, static_cast<const T0*>(a.x), a.scale,
                  static_cast<const T1*>(a.residual), a.w, a.eps, static_cast<T1*>(a.r_out),
                  static_cast<T2*>(a.out), a.M, a.D);
   return hipGetLastError();
@@ -483,10 +504,11 @@ hipError_t add_norm_fwd_t(const AddNormArgs& a, hipStream_t st) {
 
 template <typename T0, typename T1, typename T2>
 hipError_t add_norm_bwd_t(const AddNormArgs& a, hipStream_t st) {
+  const Shape shape = bwd_shape(a.D);
   const int nparts = add_norm_parts(a.M, a.D);
   float* part = static_cast<float*>(a.workspace);
   if (nparts > 0) {  // no rows: the sums are zero
-    SSD_ROW_LAUNCH(ssd_add_norm_bwd_kernel, a.D, dim3(nparts), kBwdThreads, st, static_cast<const T2*>(a.dout),
+    SSD_ROW_LAUNCH(ssd_add_norm_bwd_kernel, a.D, shape, SSD_BWD_WIDE, dim3(nparts), kBwdThreads, st, static_cast<const T2*>(a.dout),
                    static_cast<const T1*>(a.dres), static_cast<const T1*>(a.r), static_cast<const T0*>(a.x),
                    a.scale, a.w, a.eps, static_cast<T1*>(a.dresidual), static_cast<T0*>(a.dx), part, a.M, a.D,
                    static_cast<int>(a.dscale != nullptr));
@@ -499,8 +521,9 @@ hipError_t add_norm_bwd_t(const AddNormArgs& a, hipStream_t st) {
 template <typename T0, typename T1, typename T2>
 hipError_t gated_norm_fwd_t(const GatedNormArgs& a, hipStream_t st) {
   const int L = a.D / a.groups;
-  const dim3 grid(row_blocks(a.M, L, a.groups, kFwdThreads, kFwdBlocks), a.groups);
-  SSD_ROW_LAUNCH(ssd_gated_norm_kernel, L, grid, kFwdThreads, st, static_cast<const T0*>(a.y),
+  const Shape shape = fwd_shape(L);
+  const dim3 grid(row_blocks(a.M, shape, a.groups, kFwdThreads, kFwdBlocks), a.groups);
+  SSD_ROW_LAUNCH(ssd_gated_norm_kernel, L, shape, SSD_FWD_WIDE, grid, kFwdThreads, st, static_cast<const T0*>(a.y),
                  static_cast<const T1*>(a.z), a.ldz, a.w, a.eps, a.before, static_cast<T2*>(a.out), a.M, a.D, L);
   return hipGetLastError();
 }
@@ -508,10 +531,11 @@ hipError_t gated_norm_fwd_t(const GatedNormArgs& a, hipStream_t st) {
 template <typename T0, typename T1, typename T2>
 hipError_t gated_norm_bwd_t(const GatedNormArgs& a, hipStream_t st) {
   const int L = a.D / a.groups;
+  const Shape shape = bwd_shape(L);
   const int nparts = gated_norm_parts(a.M, a.D, a.groups);
   float* part = static_cast<float*>(a.workspace);
   if (nparts > 0) {
-    SSD_ROW_LAUNCH(ssd_gated_norm_bwd_kernel, L, dim3(nparts, a.groups), kBwdThreads, st,
+    SSD_ROW_LAUNCH(ssd_gated_norm_bwd_kernel, L, shape, SSD_BWD_WIDE, dim3(nparts, a.groups), kBwdThreads, st,
                    static_cast<const T2*>(a.dout), static_cast<const T0*>(a.y), static_cast<const T1*>(a.z), a.ldz,
                    a.w, a.eps, a.before, static_cast<T0*>(a.dy), static_cast<T1*>(a.dz), a.lddz, part, a.M, a.D, L);
     const hipError_t e = hipGetLastError();
@@ -542,9 +566,10 @@ hipError_t sum_parts(const float* part, int nparts, int n, float* a, int na, flo
   return hipGetLastError();
 }
 
-int add_norm_parts(int M, int D) { return row_blocks(M, D, 1, kBwdThreads, bwd_blocks(D)); }
+int add_norm_parts(int M, int D) { return row_blocks(M, bwd_shape(D), 1, kBwdThreads, bwd_blocks(D, 2)); }
 int gated_norm_parts(int M, int D, int groups) {
-  return row_blocks(M, D / groups, groups, kBwdThreads, bwd_blocks(D / groups));
+  const int L = D / groups;
+  return row_blocks(M, bwd_shape(L), groups, kBwdThreads, bwd_blocks(L, 1));
 }
 
 hipError_t run_add_norm(const AddNormArgs& a, hipStream_t st) {
