@@ -801,126 +801,46 @@ def ssd_mimo_fwd(y, W, z=None, out_dtype=torch.bfloat16, stream=None):
     return z
 
 
-_CODES = {torch.float32: SSD_F32, torch.bfloat16: SSD_BF16}
+_native_module = None
+
+
+def native():
+    """The layer operators' binding (csrc/binding.cpp), bound to the library."""
+    global _native_module
+    if _native_module is None:
+        lib()  # raises where nothing is built
+        from . import _native
+        _native.bind(LIB_PATH)
+        _native_module = _native
+    return _native_module
 
 
 def _code(dtype, name):
-    c = _CODES.get(dtype)
-    return _dcode(dtype, name) if c is None else c
+    """SSD_F32 or SSD_BF16, or -1 for None: the callee's default."""
+    return -1 if dtype is None else _dcode(dtype, name)
 
 
-class _Here:
-    """The scope of a call on the current device and its current stream."""
-
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return False
-
-
-_HERE_SCOPE = _Here()
-
-
-def _scope(t, stream):
-    """Context that makes t's device, and the call's stream on it, current, so
-    that what a call allocates belongs to the stream it runs on and the launch
-    goes to t's device."""
+def _call(fn, t, stream, *args):
+    """fn(*args, raw stream) with t's device, and the call's stream on it,
+    current, so that what the call allocates belongs to the stream it runs on
+    and the launch goes to t's device."""
     if stream is not None:
         if stream.device != t.device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
-        return torch.cuda.stream(stream)
-    if t.get_device() == torch._C._cuda_getDevice():
-        return _HERE_SCOPE
-    return torch.cuda.device(t.device)
-
-
-def _raw_stream(t):
-    """Handle of the current stream of t's device (inside its _scope)."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
-
-
-def _tensors(ref, *specs):
-    """Pointers of the arguments (tensor or None, name, shape, dtype), each of
-    exactly this shape and type and contiguous on ref's GPU."""
-    out = []
-    dev = ref.get_device()
-    for t, name, shape, dtype in specs:
-        if t is None:
-            out.append(None)
-        elif (t.shape == shape and t.dtype is dtype and t.get_device() == dev and dev >= 0
-              and t.is_contiguous()):
-            out.append(t.data_ptr())
+        with torch.cuda.stream(stream):
+            r = fn(*args, stream.cuda_stream)
+    else:
+        dev = t.get_device()
+        if dev < 0:
+            r = fn(*args, 0)  # not a GPU tensor: refused by name
+        elif dev == torch._C._cuda_getDevice():
+            r = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
         else:
-            _refuse(ref, specs)
-    return out
-
-
-def _refuse(ref, specs):
-    """Raises for the first argument that _tensors does not take: any shape or
-    type before any device or layout."""
-    for t, name, shape, dtype in specs:
-        if t is None:
-            continue
-        if t.shape != shape:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    for t, name, shape, dtype in specs:
-        if t is None:
-            continue
-        if not t.is_cuda:
-            raise ValueError(f"{name} must be a GPU tensor")
-        if t.device != ref.device:
-            raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    raise AssertionError("unreachable")
-
-
-def _rows_like(t, name, shape, dtype, ref):
-    """Shape, type and device of a strided argument (see _lead)."""
-    if t.shape != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.get_device() != ref.get_device():
-        raise ValueError(f"{name} is on {t.device}, expected {ref.device}")
-
-
-def _lead(t, name):
-    """Rows of the last axis of a tensor whose leading axes collapse into one
-    evenly spaced axis (contiguous, or a column slice of such rows): their
-    stride in elements."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a GPU tensor")
-    if t.dim() == 2 and t.shape[0] > 1 and t.stride(1) == 1 and t.stride(0) >= t.shape[1] > 0:
-        return t.stride(0)
-    if t.numel() == 0 or t.is_contiguous():
-        return max(t.shape[-1], 1)
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
-        raise ValueError(f"{name} must have a contiguous last dim")
-    ld = span = None
-    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
-        if size == 1:
-            continue
-        if ld is None:
-            ld = stride
-        elif stride != span:
-            raise ValueError(f"{name}: its rows must be evenly spaced")
-        span = stride * size
-    if ld is None:
-        return t.shape[-1]
-    if ld < t.shape[-1]:
-        raise ValueError(f"{name}: rows {ld} apart overlap, they have {t.shape[-1]} elements")
-    return ld
-
-
-def _scratch(nbytes, ref, workspace):
-    if workspace is None:
-        return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=ref.device)
-    _tensors(ref, (workspace, "workspace", workspace.shape, torch.uint8))
-    return workspace
+            with torch.cuda.device(dev):
+                r = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if r.__class__ is int:
+        _check(r)
+    return r
 
 
 def ssd_add_norm_bwd_workspace_size(M, D):
@@ -935,12 +855,6 @@ def ssd_conv1d_bwd_workspace_size(Bsz, T, HP, GN):
     return int(lib().ssd_conv1d_bwd_workspace_size(Bsz, T, HP, GN))
 
 
-def _rows_of(x, name):
-    if x.dim() < 1 or x.shape[-1] < 1:
-        raise ValueError(f"{name} must have rows of at least one channel, got shape {tuple(x.shape)}")
-    return x.shape[-1], x.numel() // x.shape[-1]
-
-
 def ssd_add_norm_fwd(x, w, residual=None, scale=None, eps=1e-5, out=None, out_dtype=None,
                      residual_out=None, res_dtype=None, stream=None):
     """Residual update and pre-norm of a block: r = residual + scale * x, out =
@@ -949,33 +863,8 @@ def ssd_add_norm_fwd(x, w, residual=None, scale=None, eps=1e-5, out=None, out_dt
     scale may be None (0, 1).  out has out_dtype (default x's), r the type of
     residual (default float32, or res_dtype); residual_out may be residual
     itself.  Returns (out, r)."""
-    D, M = _rows_of(x, "x")
-    shape = x.shape
-    xd = _code(x.dtype, "x")
-    if residual is not None:
-        if res_dtype not in (None, residual.dtype):
-            raise TypeError(f"residual is {residual.dtype}, res_dtype {res_dtype}")
-        res_dtype = residual.dtype
-    elif res_dtype is None:
-        res_dtype = torch.float32 if residual_out is None else residual_out.dtype
-    if out_dtype is None:
-        out_dtype = x.dtype if out is None else out.dtype
-    rd, od = _code(res_dtype, "residual"), _code(out_dtype, "out")
-    f32 = torch.float32
-    px, ps, pr, pw, pro, po = _tensors(
-        x, (x, "x", shape, x.dtype), (scale, "scale", (D,), f32),
-        (residual, "residual", shape, res_dtype), (w, "w", (D,), f32),
-        (residual_out, "residual_out", shape, res_dtype), (out, "out", shape, out_dtype))
-    with _scope(x, stream):
-        if out is None:
-            out = torch.empty(shape, dtype=out_dtype, device=x.device)
-            po = out.data_ptr()
-        if residual_out is None:
-            residual_out = torch.empty(shape, dtype=res_dtype, device=x.device)
-            pro = residual_out.data_ptr()
-        _check(lib().ssd_add_norm_fwd(px, ps, pr, pw, eps, pro, po, M, D, xd, rd, od,
-                                      _raw_stream(x)))
-    return out, residual_out
+    return _call(native().add_norm_fwd, x, stream, x, w, residual, scale, eps, out,
+                 _code(out_dtype, "out"), residual_out, _code(res_dtype, "residual"))
 
 
 def ssd_add_norm_bwd(dout, r, w, dres=None, scale=None, x=None, eps=1e-5, x_dtype=None,
@@ -985,27 +874,8 @@ def ssd_add_norm_bwd(dout, r, w, dres=None, scale=None, x=None, eps=1e-5, x_dtyp
     forward's, needed for dscale only).  Returns a dict: dresidual (r's type),
     dx (x_dtype; default x's type, or dout's), dw (D) float32 and dscale (D)
     float32 (None unless x is given)."""
-    D, M = _rows_of(r, "r")
-    shape = r.shape
-    if x_dtype is None:
-        x_dtype = dout.dtype if x is None else x.dtype
-    xd, rd, od = _code(x_dtype, "x"), _code(r.dtype, "r"), _code(dout.dtype, "dout")
-    f32 = torch.float32
-    pr, pd, pe, px, pw, ps = _tensors(
-        r, (r, "r", shape, r.dtype), (dout, "dout", shape, dout.dtype),
-        (dres, "dres", shape, r.dtype), (x, "x", shape, x_dtype), (w, "w", (D,), f32),
-        (scale, "scale", (D,), f32))
-    with _scope(r, stream):
-        dresidual = torch.empty(shape, dtype=r.dtype, device=r.device)
-        dx = torch.empty(shape, dtype=x_dtype, device=r.device)
-        dw = torch.empty(D, dtype=f32, device=r.device)
-        ds = None if x is None else torch.empty(D, dtype=f32, device=r.device)
-        ws = _scratch(ssd_add_norm_bwd_workspace_size(M, D), r, workspace)
-        _check(lib().ssd_add_norm_bwd(pd, pe, pr, px, ps, pw, eps, dresidual.data_ptr(),
-                                      dx.data_ptr(), dw.data_ptr(),
-                                      None if ds is None else ds.data_ptr(), M, D, xd, rd, od,
-                                      ws.data_ptr(), ws.numel(), _raw_stream(r)))
-    return dict(dresidual=dresidual, dx=dx, dw=dw, dscale=ds)
+    return _call(native().add_norm_bwd, r, stream, dout, r, w, dres, scale, x, eps,
+                 _code(x_dtype, "x"), workspace)
 
 
 def ssd_gated_norm_fwd(y, z, w, groups=1, eps=1e-5, norm_before_gate=False, out=None,
@@ -1015,22 +885,8 @@ def ssd_gated_norm_fwd(y, z, w, groups=1, eps=1e-5, norm_before_gate=False, out=
     rms(y) * w * silu(z).  y (..., D) contiguous; z of y's shape, contiguous or
     a column slice of evenly spaced rows (the in_proj rows); float32 or bfloat16
     each; w (D) float32.  Returns out (..., D) in out_dtype (default z's)."""
-    D, M = _rows_of(y, "y")
-    shape = y.shape
-    if out_dtype is None:
-        out_dtype = z.dtype if out is None else out.dtype
-    yd, zd, od = _code(y.dtype, "y"), _code(z.dtype, "z"), _code(out_dtype, "out")
-    _rows_like(z, "z", shape, z.dtype, y)
-    py, pw, po = _tensors(y, (y, "y", shape, y.dtype), (w, "w", (D,), torch.float32),
-                          (out, "out", shape, out_dtype))
-    ldz = _lead(z, "z")
-    with _scope(y, stream):
-        if out is None:
-            out = torch.empty(shape, dtype=out_dtype, device=y.device)
-            po = out.data_ptr()
-        _check(lib().ssd_gated_norm_fwd(py, z.data_ptr(), ldz, pw, eps, int(bool(norm_before_gate)),
-                                        po, M, D, groups, yd, zd, od, _raw_stream(y)))
-    return out
+    return _call(native().gated_norm_fwd, y, stream, y, z, w, groups, eps,
+                 1 if norm_before_gate else 0, out, _code(out_dtype, "out"))
 
 
 def ssd_gated_norm_bwd(dout, y, z, w, groups=1, eps=1e-5, norm_before_gate=False, dz=None,
@@ -1039,26 +895,8 @@ def ssd_gated_norm_bwd(dout, y, z, w, groups=1, eps=1e-5, norm_before_gate=False
     column slice of evenly spaced rows (the in_proj gradient's; other columns
     are left as they are).  Returns a dict: dy (y's type), dz (z's type), dw (D)
     float32."""
-    D, M = _rows_of(y, "y")
-    shape = y.shape
-    yd, zd, od = _code(y.dtype, "y"), _code(z.dtype, "z"), _code(dout.dtype, "dout")
-    _rows_like(z, "z", shape, z.dtype, y)
-    if dz is not None:
-        _rows_like(dz, "dz", shape, z.dtype, y)
-    py, pd, pw = _tensors(y, (y, "y", shape, y.dtype), (dout, "dout", shape, dout.dtype),
-                          (w, "w", (D,), torch.float32))
-    ldz = _lead(z, "z")
-    with _scope(y, stream):
-        if dz is None:
-            dz = torch.empty(shape, dtype=z.dtype, device=y.device)
-        dy = torch.empty(shape, dtype=y.dtype, device=y.device)
-        dw = torch.empty(D, dtype=torch.float32, device=y.device)
-        ws = _scratch(ssd_gated_norm_bwd_workspace_size(M, D, groups), y, workspace)
-        _check(lib().ssd_gated_norm_bwd(pd, py, z.data_ptr(), ldz, pw, eps,
-                                        int(bool(norm_before_gate)), dy.data_ptr(), dz.data_ptr(),
-                                        _lead(dz, "dz"), dw.data_ptr(), M, D, groups, yd, zd, od,
-                                        ws.data_ptr(), ws.numel(), _raw_stream(y)))
-    return dict(dy=dy, dz=dz, dw=dw)
+    return _call(native().gated_norm_bwd, y, stream, dout, y, z, w, groups, eps,
+                 1 if norm_before_gate else 0, dz, workspace)
 
 
 def ssd_conv1d_bwd(xbc, w, dx, dB, dC, bias=None, state_in=None, dstate_out=None, act=1, dxbc=None,
@@ -1070,38 +908,8 @@ def ssd_conv1d_bwd(xbc, w, dx, dB, dC, bias=None, state_in=None, dstate_out=None
     be given as a column slice of evenly spaced rows (other columns are left as
     they are).  Returns a dict: dxbc (xbc's type), dw (Ch,4), dbias (Ch) and
     dstate_in (Bsz,3,Ch; None unless want_dstate_in), float32."""
-    _ndim(xbc, "xbc", 3)
-    _ndim(dx, "dx", 3)
-    _ndim(dB, "dB", 3)
-    _ndim(w, "w", 2)
-    Bsz, T, Ch = xbc.shape
-    HP, GN, K = dx.shape[2], dB.shape[2], w.shape[1]
-    if Ch != HP + 2 * GN:
-        raise ValueError(f"xbc has {Ch} channels, HP + 2*GN = {HP + 2 * GN}")
-    code = _code(xbc.dtype, "xbc")
-    f32 = torch.float32
-    if dxbc is not None:
-        _rows_like(dxbc, "dxbc", (Bsz, T, Ch), xbc.dtype, xbc)
-    pw, px, pb, pc, pi, ps, pe = _tensors(
-        xbc, (w, "w", (Ch, K), f32), (dx, "dx", (Bsz, T, HP), xbc.dtype),
-        (dB, "dB", (Bsz, T, GN), f32), (dC, "dC", (Bsz, T, GN), f32), (bias, "bias", (Ch,), f32),
-        (state_in, "state_in", (Bsz, K - 1, Ch), f32),
-        (dstate_out, "dstate_out", (Bsz, K - 1, Ch), f32))
-    ld = _lead(xbc, "xbc")
-    dev = xbc.device
-    with _scope(xbc, stream):
-        if dxbc is None:
-            dxbc = torch.empty((Bsz, T, Ch), dtype=xbc.dtype, device=dev)
-        dw = torch.empty((Ch, K), dtype=f32, device=dev)
-        dbias = torch.empty(Ch, dtype=f32, device=dev)
-        dstate = torch.empty((Bsz, K - 1, Ch), dtype=f32, device=dev) if want_dstate_in else None
-        ws = _scratch(ssd_conv1d_bwd_workspace_size(Bsz, T, HP, GN), xbc, workspace)
-        _check(lib().ssd_conv1d_bwd(xbc.data_ptr(), ld, pw, pi, ps, int(act), px, pb, pc, pe,
-                                    dxbc.data_ptr(), _lead(dxbc, "dxbc"), dw.data_ptr(),
-                                    dbias.data_ptr(), None if dstate is None else dstate.data_ptr(),
-                                    Bsz, T, HP, GN, K, code, ws.data_ptr(), ws.numel(),
-                                    _raw_stream(xbc)))
-    return dict(dxbc=dxbc, dw=dw, dbias=dbias, dstate_in=dstate)
+    return _call(native().conv1d_bwd, xbc, stream, xbc, w, dx, dB, dC, bias, state_in, dstate_out,
+                 act, dxbc, want_dstate_in, workspace)
 
 
 def ssd_mixer_step(conv_state, h, arrivals, xbc, dt, w, A, bias=None, D=None, dt_bias=None,
@@ -1115,32 +923,5 @@ def ssd_mixer_step(conv_state, h, arrivals, xbc, dt, w, A, bias=None, D=None, dt
     outside the pool, or taken by an earlier row, is padding: its y is zero.
     xbc (Bsz,Ch) and dt (Bsz,H) float32 or bfloat16, contiguous or column slices
     of the in_proj rows.  Returns y (Bsz,H,P) in y_dtype."""
-    _ndim(h, "h", 4)
-    _ndim(xbc, "xbc", 2)
-    _ndim(w, "w", 2)
-    nslots, H, P, N = h.shape
-    Bsz, Ch = xbc.shape
-    if Ch <= H * P or (Ch - H * P) % (2 * N):
-        raise ValueError(f"xbc has {Ch} channels, not H*P + 2*G*N with H={H} P={P} N={N}")
-    G, K = (Ch - H * P) // (2 * N), w.shape[1]
-    code = _code(xbc.dtype, "xbc")
-    f32 = torch.float32
-    if y is not None:
-        y_dtype = y.dtype
-    yd = _code(y_dtype, "y")
-    _rows_like(xbc, "xbc", (Bsz, Ch), xbc.dtype, h)
-    _rows_like(dt, "dt", (Bsz, H), xbc.dtype, h)
-    ph, ps, pa, pm, pw, pA, pi, pD, pt, py = _tensors(
-        h, (h, "h", h.shape, f32), (conv_state, "conv_state", (nslots, K - 1, Ch), f32),
-        (arrivals, "arrivals", (nslots, G), torch.int32), (slots, "slots", (Bsz,), torch.int32),
-        (w, "w", (Ch, K), f32), (A, "A", (H,), f32), (bias, "bias", (Ch,), f32),
-        (D, "D", (H,), f32), (dt_bias, "dt_bias", (H,), f32), (y, "y", (Bsz, H, P), y_dtype))
-    ldx, lddt = _lead(xbc, "xbc"), _lead(dt, "dt")
-    with _scope(h, stream):
-        if y is None:
-            y = torch.empty((Bsz, H, P), dtype=y_dtype, device=h.device)
-            py = y.data_ptr()
-        _check(lib().ssd_mixer_step(ps, ph, pa, pm, nslots, xbc.data_ptr(), ldx, dt.data_ptr(), lddt,
-                                    pw, pi, int(act), pA, pD, pt, dt_min, dt_max, py, yd, Bsz, H, P,
-                                    G, N, K, code, _raw_stream(h)))
-    return y
+    return _call(native().mixer_step, h, stream, conv_state, h, arrivals, xbc, dt, w, A, bias, D,
+                 dt_bias, dt_min, dt_max, slots, act, y, _code(y_dtype, "y"))

@@ -1,13 +1,17 @@
-"""Builds libssd.so (the HIP C-ABI library) in-tree for gfx950 with hipcc."""
+"""Builds libssd.so (the HIP C-ABI library) in-tree for gfx950 with hipcc, and
+_native.so (the layer operators' binding, host code against torch's headers)
+with g++."""
 import concurrent.futures
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libssd.so")
+NATIVE = os.path.join(PKG, "_native.so")
 SOURCES = ["ssd_api.hip", "ssd_chunk.hip", "ssd_chunk_bf16.hip", "ssd_chunk_cplx.hip",
            "ssd_decode.hip", "ssd_conv.hip", "ssd_bwd_bf16.hip", "ssd_bwd_f32.hip",
            "ssd_linear.hip", "ssd_norm.hip", "ssd_conv_bwd.hip", "ssd_mixer_step.hip"]
@@ -38,11 +42,30 @@ def _compile(src, extra):
     return obj, r.stderr
 
 
+def _build_native():
+    import torch
+    from torch.utils import cpp_extension
+    inc = [f"-isystem{p}" for p in (*cpp_extension.include_paths(), sysconfig.get_paths()["include"])]
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = NATIVE + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden", "-Wall",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc,
+           os.path.join(CSRC, "binding.cpp"), "-o", tmp, f"-L{libs}", "-ltorch_python", "-ltorch_cpu",
+           "-lc10", "-ldl"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for binding.cpp:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, NATIVE)
+
+
 def build(extra_flags=(), verbose=False):
-    """Compile every HIP source and link libssd.so; returns the library path."""
+    """Compile every HIP source and link libssd.so, and the binding _native.so;
+    returns the library path."""
     os.makedirs(BUILD, exist_ok=True)
-    with concurrent.futures.ThreadPoolExecutor(len(SOURCES)) as ex:
+    with concurrent.futures.ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        native = ex.submit(_build_native)
         results = list(ex.map(lambda s: _compile(s, list(extra_flags)), SOURCES))
+        native.result()
     objs = [o for o, _ in results]
     if verbose:
         for _, err in results:
