@@ -574,8 +574,9 @@ int ssd_mimo_fwd(const void *y, int y_dtype, const void *W, void *z,
  *                        may be `residual` itself (updated in place)
  *   out          (M, D)  out_dtype, rounded once
  * M >= 0 rows of D channels, 1 <= D <= 16384, any alignment of the element
- * size.  Sums are float32: |r| stays below about 1e18 (its squares do not
- * overflow).  Apart from residual_out, outputs must not overlap inputs (such a
+ * size.  eps >= 0 (0 with a row of zeros gives NaN, as the formula does).  Sums
+ * are float32: |r| stays below about 1e18 (its squares do not overflow).  Apart
+ * from residual_out, outputs must not overlap inputs (such a
  * call is rejected).  Errors: SSD_EINVAL, SSD_EUNSUPPORTED (dtype, D), SSD_EHIP.
  */
 int ssd_add_norm_fwd(const void *x, const float *scale, const void *residual,
@@ -597,7 +598,9 @@ int ssd_add_norm_fwd(const void *x, const float *scale, const void *residual,
  *   dscale    (D)     float32, summed over the rows, or NULL
  *   workspace ssd_add_norm_bwd_workspace_size(M, D) bytes, 256-byte aligned
  * Sums over rows are made in a fixed order (no atomics): the same call gives
- * the same bits.  Outputs are overwritten and must not overlap anything.
+ * the same bits.  Outputs are overwritten and must not overlap anything.  A
+ * workspace serves one call at a time (two graphs that replay at the same time
+ * need two).
  */
 size_t ssd_add_norm_bwd_workspace_size(int M, int D);
 int ssd_add_norm_bwd(const void *dout, const void *dres, const void *r,

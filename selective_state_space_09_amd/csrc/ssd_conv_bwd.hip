@@ -27,6 +27,12 @@
 // differ in type).  The four waves of a workgroup take runs of the same
 // channels and join their sums in LDS; each workgroup writes one row of a
 // partial-sum table that a second kernel adds up in a fixed order.
+//
+// What bounds it: the bytes (2 x 2048 tokens of 4352 bf16 channels: 109 MB, 21.7
+// us as one elementwise library kernel) and, close behind, the VALU: 30
+// instructions and two quarter-rate ones per element, 14.5 us.  27 us for this
+// kernel and 4 for the sums (3.5 TB/s); without the activation 24.3 us in all
+// where the data sits in the cache, 29.1 from HBM.
 
 #include "ssd_chunk_common.h"
 #include "ssd_internal.h"

@@ -15,11 +15,26 @@
 //
 // All of it streams: about 10 flops per element against 6 to 18 bytes, so HBM
 // bounds it.  A team of TPR lanes owns a row segment and holds it in registers
-// (K vectors of 8 elements per lane), so every input is read once: one pass
-// for the sum of squares and, from the registers, the normalised values.  The
-// sums over rows (dw, dscale) stay in registers while a team walks its rows;
-// teams of a workgroup join them in LDS and write one row of a partial-sum
-// table, which a second kernel adds up in a fixed order.
+// (K vectors of 8 elements per lane), so every input is read once, all of a
+// row's loads issued before the first is used: the sum of squares is taken and
+// the values are normalised from the same registers.  Sums, statistics and the
+// residual are float32; the norm is taken of r before it is rounded to the
+// residual's type, and each output is rounded once.  The sums over rows (dw,
+// dscale) stay in registers while a team walks its rows; teams of a workgroup
+// join them in LDS and write one row of a partial-sum table, which a second
+// kernel adds up in a fixed order (no atomics).
+//
+// Measured (a 1 GiB copy reaches 4.98 TB/s, a 64 MB one in the cache 6.8):
+//   residual norm, 16384 x 2048, bf16 x and out, float32 r:  82.7 us, 4.87 TB/s
+//     backward, 4096 x 2048, with dscale:  38.1 us in all, 33 + 4.8 us for the
+//     sums (3.97 TB/s; two library adds over the same bytes take 31.1 us)
+//     backward, 1237 x 1027, float32:  15.3 us, 12 + 4 (in the cache)
+//     one row of 2048:  2.4 us (a launch)
+//   gated norm, 4096 x 4096 bf16, z in rows of 8512:  17.8 us, 5.65 TB/s
+//     backward in 8 groups:  39.5 us in all, 35.5 + 4 (4.25 TB/s)
+//     256 x 4096, float32 y:  3.5 us
+// Set aside: the next row's loads issued before a row is processed (residual
+// backward 37.5 -> 36.9 us, gated 39.9 -> 42.5: its registers cost waves).
 
 #include "ssd_chunk_common.h"
 #include "ssd_internal.h"
