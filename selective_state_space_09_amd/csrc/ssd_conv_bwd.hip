@@ -30,9 +30,8 @@
 //
 // What bounds it: the bytes (2 x 2048 tokens of 4352 bf16 channels: 109 MB, 21.7
 // us as one elementwise library kernel) and, close behind, the VALU: 30
-// instructions and two quarter-rate ones per element, 14.5 us.  27 us for this
-// kernel and 4 for the sums (3.5 TB/s); without the activation 24.3 us in all
-// where the data sits in the cache, 29.1 from HBM.
+// instructions per element, two of them quarter-rate, 14.5 us.  24 us for this
+// kernel and 4 for the sums: 28.1 us, 3.9 TB/s.
 
 #include "ssd_chunk_common.h"
 #include "ssd_internal.h"
@@ -43,7 +42,7 @@ namespace ssd {
 namespace {
 
 // Measured at 2 x 2048 tokens of 4352 bf16 channels (both kernels; the whole
-// call's bytes as one elementwise library kernel: 21.7 us): V = 2, runs of 32,
+// call's bytes as one elementwise library kernel: 21.7 us), runs of 32: V = 2,
 // blocks of 4 31.4 us, blocks of 8 34.3; with a second copy of the block's code
 // for its last tokens 33.4 (4) and 32.0 (8); one descriptor per run and the row
 // in the lane's offset 34.4 (8); V = 4 42.9 (half the waves).
@@ -99,7 +98,7 @@ __device__ __forceinline__ void conv_bwd_body(
     float* __restrict__ dstate_in, int Bsz, int Tn, int Ch, int c, int cr, int W, bool active,
     int run, long long first, long long stride, float (&dw)[kV][4], float (&db)[kV]) {
   constexpr int V = kV;
-  const int nruns = Tn > 0 ? (Tn + run - 1) / run : 1;
+  const int nruns = Tn > 0 ? (Tn - 1) / run + 1 : 1;
   const long long units = static_cast<long long>(Bsz) * nruns;
   float wt[V][4], bs[V];
 #pragma unroll
@@ -314,23 +313,35 @@ __global__ __launch_bounds__(kThreads) void ssd_conv1d_bwd_kernel(
   }
 }
 
-// Run length and workgroups of a call: the longest run (least halo) that still
-// gives kMinWaves waves, four per SIMD.  Measured at 3 x 509 tokens of 1024 + 2 x
-// 1024 float32 channels with blocks of 8: runs of 32 (1152 waves) 19.4 us, of 16
-// 18.5, of 8 17.2.
+// Run length and workgroups of a call.  A run of n tokens costs about n + 5 (its
+// halo: three more gradients, six more rows), and the CU with the most
+// workgroups ends last, so of the runs that give kMinWaves waves (four per SIMD)
+// the one with the least ceil(workgroups / CUs) (n + 5); without enough waves
+// the shortest.  Measured (both kernels): 2 x 2048 tokens of 4352 bf16 channels,
+// 1258 workgroups of 28-token runs 28.1 us, 1088 of 32 30.0 (five on some CUs,
+// 4.25 on average), 1768 of 20 29.1; 3 x 509 tokens of 1024 + 2 x 1024 float32
+// channels, runs of 8 (4608 waves) 16.4, of 12 17.0, of 32 18.5.
 constexpr long long kMinWaves = 4096;
-constexpr int kRunMin = 8;
+constexpr int kRunMin = 8, kCUs = 256;
 struct Plan {
   int run, blocks, parts;
 };
 Plan plan_of(int Bsz, int T, int HP, int GN) {
   Plan p;
   p.blocks = region_blocks(HP) + 2 * region_blocks(GN);
-  auto units = [&](int run) { return static_cast<long long>(Bsz) * (T > 0 ? (T + run - 1) / run : 1); };
-  p.run = kRunMax;
-  while (p.run > kRunMin && p.blocks * units(p.run) < kMinWaves) p.run /= 2;
-  const long long need = (units(p.run) + 3) / 4;
-  p.parts = static_cast<int>(need < kMaxParts ? need : kMaxParts);
+  p.run = kRunMin;
+  long long best = -1, groups = 0;
+  for (int run = kRunMin; run <= kRunMax; run += kBlk) {
+    const long long units = static_cast<long long>(Bsz) * (T > 0 ? (T - 1) / run + 1 : 1);
+    const long long wgs = (units + 3) / 4;
+    const long long cost = (wgs * p.blocks + kCUs - 1) / kCUs * (run + 5);
+    if (run == kRunMin || (units * p.blocks >= kMinWaves && cost < best)) {
+      p.run = run;
+      best = cost;
+      groups = wgs;
+    }
+  }
+  p.parts = static_cast<int>(groups < kMaxParts ? groups : kMaxParts);
   return p;
 }
 
