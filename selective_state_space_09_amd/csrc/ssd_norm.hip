@@ -124,7 +124,7 @@ __global__ __launch_bounds__(team_block<TPR>(kFwdThreads)) void ssd_add_norm_ker
     if (scale) {
       Row8<float> sv[K];
 #pragma unroll
-      for (int k = 0; k < K; ++k) sv[k] = row_load<SHORT>(reload(scale), pl[k], D);
+      for (int k = 0; k < K; ++k) sv[k] = row_load<SHORT>(reload<(K > 1)>(scale), pl[k], D);
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -140,7 +140,7 @@ __global__ __launch_bounds__(team_block<TPR>(kFwdThreads)) void ssd_add_norm_ker
         for (int i = 0; i < 8; ++i) r[k][i] += rv[k][i];
     }
 #pragma unroll
-    for (int k = 0; k < K; ++k) wv[k] = row_load<SHORT>(reload(w), pl[k], D);
+    for (int k = 0; k < K; ++k) wv[k] = row_load<SHORT>(reload<(K > 1)>(w), pl[k], D);
     float ss[1] = {0.0f};
 #pragma unroll
     for (int k = 0; k < K; ++k) own_sum(ss[0], pl[k].drop, [&](int i) { return r[k][i] * r[k][i]; });
@@ -224,7 +224,7 @@ __global__ __launch_bounds__(team_block<TPR>(kBwdThreads)) void ssd_add_norm_bwd
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const Row8<float> wv = row_load<SHORT>(reload(w), pl[k], D);
+      const Row8<float> wv = row_load<SHORT>(reload<(K > 1)>(w), pl[k], D);
       own_sum(s[0], pl[k].drop, [&](int i) { return rv[k][i] * rv[k][i]; });
       own_sum(s[1], pl[k].drop, [&](int i) { return dv[k][i] * wv[i] * rv[k][i]; });
     }
@@ -234,9 +234,9 @@ __global__ __launch_bounds__(team_block<TPR>(kBwdThreads)) void ssd_add_norm_bwd
     const float m = s[1] * rstd * inv;  // mean(dn o n)
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      remake(rv[k]);
-      remake(dv[k]);
-      const Row8<float> wv = row_load<SHORT>(reload(w), pl[k], D);
+      remake<(K > 1)>(rv[k]);
+      remake<(K > 1)>(dv[k]);
+      const Row8<float> wv = row_load<SHORT>(reload<(K > 1)>(w), pl[k], D);
       float g[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -252,7 +252,7 @@ __global__ __launch_bounds__(team_block<TPR>(kBwdThreads)) void ssd_add_norm_bwd
       }
       if (dx) {
         if (scale) {
-          const Row8<float> sv = row_load<SHORT>(reload(scale), pl[k], D);
+          const Row8<float> sv = row_load<SHORT>(reload<(K > 1)>(scale), pl[k], D);
 #pragma unroll
           for (int i = 0; i < 8; ++i) g[i] *= sv[i];
         }
@@ -291,7 +291,7 @@ __global__ __launch_bounds__(team_block<TPR>(kFwdThreads)) void ssd_gated_norm_k
       zv[k] = row_load<SHORT>(z + static_cast<size_t>(row) * ldz + c0, pl[k], L);
     }
 #pragma unroll
-    for (int k = 0; k < K; ++k) wv[k] = row_load<SHORT>(reload(w) + c0, pl[k], L);
+    for (int k = 0; k < K; ++k) wv[k] = row_load<SHORT>(reload<(K > 1)>(w) + c0, pl[k], L);
     float u[K][8], gt[K][8];
     float ss[1] = {0.0f};
 #pragma unroll
@@ -348,7 +348,7 @@ __global__ __launch_bounds__(team_block<TPR>(kBwdThreads)) void ssd_gated_norm_b
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const Row8<float> wv = row_load<SHORT>(reload(w) + c0, pl[k], L);
+      const Row8<float> wv = row_load<SHORT>(reload<(K > 1)>(w) + c0, pl[k], L);
       float u[8], dn[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -365,10 +365,10 @@ __global__ __launch_bounds__(team_block<TPR>(kBwdThreads)) void ssd_gated_norm_b
     const float m = s[1] * rstd * inv;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      remake(yv[k]);
-      remake(zv[k]);
-      remake(dv[k]);
-      const Row8<float> wv = row_load<SHORT>(reload(w) + c0, pl[k], L);
+      remake<(K > 1)>(yv[k]);
+      remake<(K > 1)>(zv[k]);
+      remake<(K > 1)>(dv[k]);
+      const Row8<float> wv = row_load<SHORT>(reload<(K > 1)>(w) + c0, pl[k], L);
       float gy[8], gz[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
