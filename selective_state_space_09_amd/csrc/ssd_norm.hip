@@ -25,16 +25,17 @@
 // kernel adds up in a fixed order (no atomics).
 //
 // Measured (a 1 GiB copy reaches 4.98 TB/s, a 64 MB one in the cache 6.8):
-//   residual norm, 16384 x 2048, bf16 x and out, float32 r:  82.7 us, 4.87 TB/s
-//     backward, 4096 x 2048, with dscale:  38.1 us in all, 33 + 4.8 us for the
-//     sums (3.97 TB/s; two library adds over the same bytes take 31.1 us)
-//     backward, 1237 x 1027, float32:  15.3 us, 12 + 4 (in the cache)
+//   residual norm, 16384 x 2048, bf16 x and out, float32 r:  78.9 us, 5.1 TB/s
+//     backward, 4096 x 2048, with dscale:  32.7 us in all, 28 + 4.5 us for the
+//     sums (4.6 TB/s; two library adds over the same bytes take 31.1 us)
+//     backward, 1237 x 1027, float32:  13.6 us, 10 + 4 (in the cache)
 //     one row of 2048:  2.4 us (a launch)
-//   gated norm, 4096 x 4096 bf16, z in rows of 8512:  17.8 us, 5.65 TB/s
-//     backward in 8 groups:  39.5 us in all, 35.5 + 4 (4.25 TB/s)
-//     256 x 4096, float32 y:  3.5 us
+//   gated norm, 4096 x 4096 bf16, z in rows of 8512:  17.4 us, 5.8 TB/s
+//     backward in 8 groups:  34.3 us in all (4.9 TB/s)
+//     256 x 4096, float32 y:  3.4 us
 // Set aside: the next row's loads issued before a row is processed (residual
-// backward 37.5 -> 36.9 us, gated 39.9 -> 42.5: its registers cost waves).
+// backward 37.5 -> 36.9 us, gated 39.9 -> 42.5, before the weights stayed in
+// registers).
 
 #include "ssd_chunk_common.h"
 #include "ssd_internal.h"
@@ -158,6 +159,11 @@ __global__ __launch_bounds__(team_block<TPR>(kFwdThreads)) void ssd_add_norm_ker
   }
 }
 
+// Backward: what is loaded or made again rather than kept (see reload, remake):
+// where two vectors a lane meet 128 registers.
+template <int TPR, int K>
+constexpr bool kHide = K > 1 && TPR > kWave;
+
 // The team's column sums (K vectors of 8 per lane) joined over the workgroup's
 // teams and written as columns 0 .. L-1 of `part`.
 template <int TPR, int K, bool SHORT>
@@ -224,7 +230,7 @@ __global__ __launch_bounds__(team_block<TPR>(kBwdThreads)) void ssd_add_norm_bwd
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const Row8<float> wv = row_load<SHORT>(reload<(K > 1)>(w), pl[k], D);
+      const Row8<float> wv = row_load<SHORT>(reload<kHide<TPR, K>>(w), pl[k], D);
       own_sum(s[0], pl[k].drop, [&](int i) { return rv[k][i] * rv[k][i]; });
       own_sum(s[1], pl[k].drop, [&](int i) { return dv[k][i] * wv[i] * rv[k][i]; });
     }
@@ -234,9 +240,9 @@ __global__ __launch_bounds__(team_block<TPR>(kBwdThreads)) void ssd_add_norm_bwd
     const float m = s[1] * rstd * inv;  // mean(dn o n)
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      remake<(K > 1)>(rv[k]);
-      remake<(K > 1)>(dv[k]);
-      const Row8<float> wv = row_load<SHORT>(reload<(K > 1)>(w), pl[k], D);
+      remake<kHide<TPR, K>>(rv[k]);
+      remake<kHide<TPR, K>>(dv[k]);
+      const Row8<float> wv = row_load<SHORT>(reload<kHide<TPR, K>>(w), pl[k], D);
       float g[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -252,7 +258,7 @@ __global__ __launch_bounds__(team_block<TPR>(kBwdThreads)) void ssd_add_norm_bwd
       }
       if (dx) {
         if (scale) {
-          const Row8<float> sv = row_load<SHORT>(reload<(K > 1)>(scale), pl[k], D);
+          const Row8<float> sv = row_load<SHORT>(reload<kHide<TPR, K>>(scale), pl[k], D);
 #pragma unroll
           for (int i = 0; i < 8; ++i) g[i] *= sv[i];
         }
@@ -348,7 +354,7 @@ __global__ __launch_bounds__(team_block<TPR>(kBwdThreads)) void ssd_gated_norm_b
     float s[2] = {0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const Row8<float> wv = row_load<SHORT>(reload<(K > 1)>(w) + c0, pl[k], L);
+      const Row8<float> wv = row_load<SHORT>(reload<kHide<TPR, K>>(w) + c0, pl[k], L);
       float u[8], dn[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -365,10 +371,10 @@ __global__ __launch_bounds__(team_block<TPR>(kBwdThreads)) void ssd_gated_norm_b
     const float m = s[1] * rstd * inv;
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      remake<(K > 1)>(yv[k]);
-      remake<(K > 1)>(zv[k]);
-      remake<(K > 1)>(dv[k]);
-      const Row8<float> wv = row_load<SHORT>(reload<(K > 1)>(w) + c0, pl[k], L);
+      remake<kHide<TPR, K>>(yv[k]);
+      remake<kHide<TPR, K>>(zv[k]);
+      remake<kHide<TPR, K>>(dv[k]);
+      const Row8<float> wv = row_load<SHORT>(reload<kHide<TPR, K>>(w) + c0, pl[k], L);
       float gy[8], gz[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -425,15 +431,21 @@ __global__ __launch_bounds__(kSumWaves* kWave) void ssd_sum_parts_kernel(
   }
 }
 
-// Lanes of a team and vectors per lane for a row segment of L elements.
 struct Shape {
   int tpr, k;
 };
+// Lanes of a team and vectors per lane for a row segment of L elements.
 // Forward: one vector per lane up to 8192 elements.  The few instructions per
 // wave set the time of a small batch (one row of 2048: 256 lanes 2.7 us, 64
 // lanes of four vectors 3.4), and large batches stream either way (4096 x 2048:
 // 17.1 and 16.9 us; 512 x 16384: 19.7 and, with 512 lanes of four, 17.5).
-Shape fwd_shape(int L) {
+// Backward: each lane also holds the column sums of its vectors.  Measured for
+// the residual norm (bf16 x and dout, float32 r and dres, 2^23 elements) and,
+// after the slash, the gated one (bf16, 2^24), floors 30.3 / 33.7 us: L = 512
+// 32.6 / 33.4 us; 1024 with 64 lanes of two 33.1 / 34.0, 128 of one 35.0 / 42.1;
+// 2048 32.2 / 36.5; 4096 34.7 / 36.6; 8192 with 1024 of one 37.3 / 41.0, 512 of
+// two 44.5 / 44.1; 16384 with 1024 of two 44.1, 512 of four 45.8.
+Shape shape_of(int L) {
   if (L <= 128) return {16, 1};
   if (L <= 512) return {64, 1};
   if (L <= 1024) return {64, 2};
@@ -442,23 +454,6 @@ Shape fwd_shape(int L) {
   if (L <= 8192) return {1024, 1};
   return {1024, 2};
 }
-// Backward: each lane also holds the column sums of its vectors.  Measured for
-// the residual norm (bf16 x and dout, float32 r and dres, 2^23 elements) and,
-// after the slash, the gated one (bf16, 2^24): L = 2048 with 256 lanes of one
-// vector 37.5 / 44.5 us, 64 of four 38.9 / 47.6; 4096 with 512 of one 37.6 /
-// 46.4, 256 of two 41.0 / 49.5; 8192 with 512 of two 45.4 / 45.8, 256 of four
-// 44.4 / 52.6, 1024 of one 44.3 / 49.1; 16384 with 512 of four 46.7, 1024 of
-// two 55.9.
-Shape bwd_shape(int L) {
-  if (L <= 128) return {16, 1};
-  if (L <= 512) return {64, 1};
-  if (L <= 1024) return {64, 2};
-  if (L <= 2048) return {256, 1};
-  if (L <= 4096) return {512, 1};
-  if (L <= 8192) return {512, 2};
-  return {512, 4};
-}
-
 // workgroups of `several` threads (or one team) along the rows: enough for
 // every row, at most `cap` over all groups
 int row_blocks(int M, Shape s, int groups, int several, int cap) {
@@ -469,13 +464,14 @@ int row_blocks(int M, Shape s, int groups, int several, int cap) {
 }
 constexpr int kFwdBlocks = 4096;
 // Backward: every workgroup writes a row of `sums` vectors of partial sums, so
-// few are wanted, but their waves have to keep the memory busy: 512, except
-// 1024 where teams of four waves write one sum (4096 x 2 norms of 2048: 44.2
-// us, at 512 47.9; the residual norm's two sums there: 38.7 and 37.5), and 256
-// of the widest (512 x 16384: 46.7 us, at 512 58.8).
+// few are wanted, but their waves have to keep the memory busy: 512; 256 with
+// two vectors a lane (8192 rows of 1024: residual norm 33.1 us, gated 34.0 at
+// 16384 rows; at 512 36.4 and 38.0) or sixteen waves (1024 x 8192: 37.3 and, at
+// 512, 42.8); 1024 where teams of four waves write one sum (4096 x 2 norms of
+// 2048: 37.1 us, at 512 40.6; the residual norm's two sums there 36.7 and 32.5).
 int bwd_blocks(int L, int sums) {
-  const Shape s = bwd_shape(L);
-  return s.tpr == 256 && sums == 1 ? 1024 : s.k == 4 ? 256 : 512;
+  const Shape s = shape_of(L);
+  return s.k == 2 || s.tpr == 1024 ? 256 : s.tpr == 256 && sums == 1 ? 1024 : 512;
 }
 
 // KERNEL<TPR, K, SHORT, types> for segments of L elements
@@ -484,34 +480,29 @@ int bwd_blocks(int L, int sums) {
     launch_k(true, KERNEL<TPR, K, false, T0, T1, T2>, grid, dim3(team_block<TPR>(several)), st, \
              nullptr, __VA_ARGS__);                                                            \
     break;
-#define SSD_ROW_LAUNCH(KERNEL, L, shape, WIDE, grid, several, st, ...)                            \
+#define SSD_ROW_LAUNCH(KERNEL, L, grid, several, st, ...)                                         \
   do {                                                                                            \
     if (L < 8) {                                                                                  \
       launch_k(true, KERNEL<16, 1, true, T0, T1, T2>, grid, dim3(team_block<16>(several)), st,     \
                nullptr, __VA_ARGS__);                                                             \
       break;                                                                                      \
     }                                                                                             \
+    const Shape shape = shape_of(L);                                                              \
     switch (shape.tpr * 8 + shape.k) {                                                            \
       SSD_ROW_CASE(KERNEL, 16, 1, grid, several, st, __VA_ARGS__)                                 \
       SSD_ROW_CASE(KERNEL, 64, 1, grid, several, st, __VA_ARGS__)                                 \
       SSD_ROW_CASE(KERNEL, 64, 2, grid, several, st, __VA_ARGS__)                                 \
       SSD_ROW_CASE(KERNEL, 256, 1, grid, several, st, __VA_ARGS__)                                \
       SSD_ROW_CASE(KERNEL, 512, 1, grid, several, st, __VA_ARGS__)                                \
-      WIDE(KERNEL, grid, several, st, __VA_ARGS__)                                                \
+      SSD_ROW_CASE(KERNEL, 1024, 1, grid, several, st, __VA_ARGS__)                               \
+      SSD_ROW_CASE(KERNEL, 1024, 2, grid, several, st, __VA_ARGS__)                               \
     }                                                                                             \
   } while (0)
-#define SSD_FWD_WIDE(KERNEL, grid, several, st, ...)               \
-  SSD_ROW_CASE(KERNEL, 1024, 1, grid, several, st, __VA_ARGS__)    \
-  SSD_ROW_CASE(KERNEL, 1024, 2, grid, several, st, __VA_ARGS__)
-#define SSD_BWD_WIDE(KERNEL, grid, several, st, ...)               \
-  SSD_ROW_CASE(KERNEL, 512, 2, grid, several, st, __VA_ARGS__)     \
-  SSD_ROW_CASE(KERNEL, 512, 4, grid, several, st, __VA_ARGS__)
 
 template <typename T0, typename T1, typename T2>
 hipError_t add_norm_fwd_t(const AddNormArgs& a, hipStream_t st) {
-  const Shape shape = fwd_shape(a.D);
-  const dim3 grid(row_blocks(a.M, shape, 1, kFwdThreads, kFwdBlocks));
-  SSD_ROW_LAUNCH(ssd_add_norm_kernel, a.D, shape, SSD_FWD_WIDE, grid, kFwdThreads, st, static_cast<const T0*>(a.x), a.scale,
+  const dim3 grid(row_blocks(a.M, shape_of(a.D), 1, kFwdThreads, kFwdBlocks));
+  SSD_ROW_LAUNCH(ssd_add_norm_kernel, a.D, grid, kFwdThreads, st, static_cast<const T0*>(a.x), a.scale,
                  static_cast<const T1*>(a.residual), a.w, a.eps, static_cast<T1*>(a.r_out),
                  static_cast<T2*>(a.out), a.M, a.D);
   return hipGetLastError();
@@ -519,11 +510,10 @@ hipError_t add_norm_fwd_t(const AddNormArgs& a, hipStream_t st) {
 
 template <typename T0, typename T1, typename T2>
 hipError_t add_norm_bwd_t(const AddNormArgs& a, hipStream_t st) {
-  const Shape shape = bwd_shape(a.D);
   const int nparts = add_norm_parts(a.M, a.D);
   float* part = static_cast<float*>(a.workspace);
   if (nparts > 0) {  // no rows: the sums are zero
-    SSD_ROW_LAUNCH(ssd_add_norm_bwd_kernel, a.D, shape, SSD_BWD_WIDE, dim3(nparts), kBwdThreads, st, static_cast<const T2*>(a.dout),
+    SSD_ROW_LAUNCH(ssd_add_norm_bwd_kernel, a.D, dim3(nparts), kBwdThreads, st, static_cast<const T2*>(a.dout),
                    static_cast<const T1*>(a.dres), static_cast<const T1*>(a.r), static_cast<const T0*>(a.x),
                    a.scale, a.w, a.eps, static_cast<T1*>(a.dresidual), static_cast<T0*>(a.dx), part, a.M, a.D,
                    static_cast<int>(a.dscale != nullptr));
@@ -536,9 +526,8 @@ hipError_t add_norm_bwd_t(const AddNormArgs& a, hipStream_t st) {
 template <typename T0, typename T1, typename T2>
 hipError_t gated_norm_fwd_t(const GatedNormArgs& a, hipStream_t st) {
   const int L = a.D / a.groups;
-  const Shape shape = fwd_shape(L);
-  const dim3 grid(row_blocks(a.M, shape, a.groups, kFwdThreads, kFwdBlocks), a.groups);
-  SSD_ROW_LAUNCH(ssd_gated_norm_kernel, L, shape, SSD_FWD_WIDE, grid, kFwdThreads, st, static_cast<const T0*>(a.y),
+  const dim3 grid(row_blocks(a.M, shape_of(L), a.groups, kFwdThreads, kFwdBlocks), a.groups);
+  SSD_ROW_LAUNCH(ssd_gated_norm_kernel, L, grid, kFwdThreads, st, static_cast<const T0*>(a.y),
                  static_cast<const T1*>(a.z), a.ldz, a.w, a.eps, a.before, static_cast<T2*>(a.out), a.M, a.D, L);
   return hipGetLastError();
 }
@@ -546,11 +535,10 @@ hipError_t gated_norm_fwd_t(const GatedNormArgs& a, hipStream_t st) {
 template <typename T0, typename T1, typename T2>
 hipError_t gated_norm_bwd_t(const GatedNormArgs& a, hipStream_t st) {
   const int L = a.D / a.groups;
-  const Shape shape = bwd_shape(L);
   const int nparts = gated_norm_parts(a.M, a.D, a.groups);
   float* part = static_cast<float*>(a.workspace);
   if (nparts > 0) {
-    SSD_ROW_LAUNCH(ssd_gated_norm_bwd_kernel, L, shape, SSD_BWD_WIDE, dim3(nparts, a.groups), kBwdThreads, st,
+    SSD_ROW_LAUNCH(ssd_gated_norm_bwd_kernel, L, dim3(nparts, a.groups), kBwdThreads, st,
                    static_cast<const T2*>(a.dout), static_cast<const T0*>(a.y), static_cast<const T1*>(a.z), a.ldz,
                    a.w, a.eps, a.before, static_cast<T0*>(a.dy), static_cast<T1*>(a.dz), a.lddz, part, a.M, a.D, L);
     const hipError_t e = hipGetLastError();
@@ -581,10 +569,10 @@ hipError_t sum_parts(const float* part, int nparts, int n, float* a, int na, flo
   return hipGetLastError();
 }
 
-int add_norm_parts(int M, int D) { return row_blocks(M, bwd_shape(D), 1, kBwdThreads, bwd_blocks(D, 2)); }
+int add_norm_parts(int M, int D) { return row_blocks(M, shape_of(D), 1, kBwdThreads, bwd_blocks(D, 2)); }
 int gated_norm_parts(int M, int D, int groups) {
   const int L = D / groups;
-  return row_blocks(M, bwd_shape(L), groups, kBwdThreads, bwd_blocks(L, 1));
+  return row_blocks(M, shape_of(L), groups, kBwdThreads, bwd_blocks(L, 1));
 }
 
 hipError_t run_add_norm(const AddNormArgs& a, hipStream_t st) {
