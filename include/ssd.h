@@ -693,7 +693,7 @@ int ssd_conv1d_bwd(const void *xbc, long long ld, const float *w,
  *   A, D, dt_bias, dt_min, dt_max      as in ssd_step_decode
  *   y          (Bsz, H, P) y_dtype
  * Both states of every named slot are updated in place.  P <= 1024, N in {16,
- * 32, 64, 128, 256}, K = 4; h and w 16-byte aligned.  Calls that share no slot
+ * 32, 64, 128, 256}, K = 4, Bsz H <= 2^23; h and w 16-byte aligned.  Calls that share no slot
  * may run at the same time; calls that share one must be ordered.  No
  * workspace.  Arrays that are written must not overlap any other.
  */

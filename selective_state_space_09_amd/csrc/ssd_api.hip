@@ -1075,7 +1075,9 @@ int ssd_mixer_step(float* conv_state, float* h, int* arrivals, const int* slots,
   if (act != 0 && act != 1) return fail(SSD_EINVAL, "act=%d not in {0, 1}", act);
   if (!slots && Bsz > nslots)
     return fail(SSD_EINVAL, "Bsz=%d rows without a slot map, nslots=%d", Bsz, nslots);
-  if (static_cast<long long>(Bsz) * H > 2147483647LL) return fail(SSD_EUNSUPPORTED, "Bsz*H too large");
+  // a launch holds below 2^32 threads, and a head has up to 320 of them
+  if (static_cast<long long>(Bsz) * H > (1LL << 23))
+    return fail(SSD_EUNSUPPORTED, "Bsz*H = %lld, at most 2^23", static_cast<long long>(Bsz) * H);
   const size_t Ch = static_cast<size_t>(H) * P + 2 * static_cast<size_t>(G) * N;
   if (Ch > (1u << 24)) return fail(SSD_EUNSUPPORTED, "%zu channels, at most 2^24", Ch);
   if (ldx < static_cast<long long>(Ch) || ldx > (1LL << 40))
