@@ -363,6 +363,7 @@ PyObject* conv1d_bwd(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Opt bias = opt(a[5], "bias"), si = opt(a[6], "state_in"), dso = opt(a[7], "dstate_out"), dxbc = opt(a[9], "dxbc");
     Opt given = opt(a[11], "workspace");
     const int act = as_int32(a[8], "act"), want = PyObject_IsTrue(a[10]);
+    if (want < 0) throw Refused{nullptr, ""};
     ndim(xbc, "xbc", 3);
     ndim(dx, "dx", 3);
     ndim(dB, "dB", 3);

@@ -201,3 +201,8 @@ def test_binding_has_no_cpu_path(fn, args):
 @pytest.mark.parametrize("B,H", [((1 << 22) + 1, 2), (2, 1 << 23)])
 def test_mixer_step_refuses_a_batch_past_one_grid(B, H):
     refuse("ssd_mixer_step", STEP, dict(B=B, H=H, P=1, ldx=H + 32, lddt=H, nslots=B), EUNSUP, "2^23")
+
+
+def test_binding_passes_on_an_error_of_a_truth_value():
+    with pytest.raises(RuntimeError, match="ambiguous"):
+        ssd.ssd_conv1d_bwd(**conv_args(), want_dstate_in=z(2))
