@@ -30,6 +30,11 @@
 // the repeated B and C: 8 rows of 64 heads in one group 9.9 us, with one head
 // 12.3 us; one row 6.5 and 6.2.
 //
+// A row looks through the slots of the rows before it (no workspace, no second
+// launch); past 256 rows in vectors of four, eight in flight: 4096 rows of
+// H = P = 64, N = 128 2976 us, without a slot map 2797, with one load at a time
+// 3631; 16384 rows of H = 8, P = 32, N = 16 767, 492 and 2521.
+//
 // Measured at 256 rows of H = P = 64, N = 128, one group (1.11 GB): 189 us, 5.9
 // TB/s; ssd_conv1d_step and ssd_step_decode on the same states in slot order
 // take 6.0 + 178 us.
@@ -42,6 +47,7 @@ namespace ssd {
 namespace {
 
 typedef float f4v __attribute__((ext_vector_type(4)));
+typedef int i4_e4 __attribute__((ext_vector_type(4), aligned(4)));  // at any element
 
 template <typename T>
 __device__ __forceinline__ float elem(T v);
@@ -115,8 +121,20 @@ __global__ __launch_bounds__(kThreads* HB + kWave) void ssd_mixer_step_kernel(
     int skip = named != slot;
 #pragma unroll
     for (int k = 0; k < FI; ++k) skip |= slots && lane + k * kWave < b && first[k] == named;
-    if (slots)
-      for (int j = lane + FI * kWave; j < b; j += kWave) skip |= slots[j] == named;
+    if (slots) {  // the rest, b >= FI kWave: vectors of four, the last ones shifted back into the rows before b
+      constexpr int U = 8;
+#pragma unroll 1
+      for (int j0 = FI * kWave; j0 < b; j0 += U * 4 * kWave) {
+        i4_e4 q[U];
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+          q[k] = *reinterpret_cast<const i4_e4*>(slots + min(j0 + (k * kWave + lane) * 4, b - 4));
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) skip |= q[k][i] == named;
+      }
+    }
     skip = __any(skip);
     if (lane == 0) padding = skip;
     __syncthreads();

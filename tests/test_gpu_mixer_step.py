@@ -192,3 +192,41 @@ def test_empty_batch_and_all_padding():
                            slots=torch.full((3,), -1, dtype=torch.int32, device="cuda"))
     assert float(y.abs().max()) == 0.0
     assert torch.equal(h, h0) and torch.equal(conv, c0)
+
+
+@pytest.mark.parametrize("B", [257, 258, 260, 511, 2304, 2305, 5003])
+def test_repeated_slots_of_long_batches(B):
+    """A row whose slot an earlier row has is padding wherever the two stand:
+    the same bits as with the later rows' slots set outside the pool."""
+    print(f"mixer_step repeated slots B={B}", flush=True)
+    H, P, G, N, ns = 2, 4, 1, 16, B
+    Ch = H * P + 2 * G * N
+    rng = np.random.default_rng(B)
+    m = rng.permutation(B)
+    for i, j in ((0, B - 1), (3, 256), (255, B - 2), (252, B - 3), (B - 5, B - 4), (7, 128)):  # pairs at the edges
+        m[j] = m[i]
+    some = rng.random(B) < 0.1
+    some[[0, 3, 7, 252, 255, B - 5]] = False
+    m = np.where(some, rng.integers(-2, ns + 2, B), m)  # others anywhere, and outside
+    once = m.copy()
+    seen = set()
+    for b, s in enumerate(m):
+        if s in seen:
+            once[b] = -1
+        seen.add(s)
+    assert (once != m).sum() >= 4 and (once >= 0).sum() > B // 2
+    torch.manual_seed(B)
+    dev = dict(device="cuda")
+    conv, h = torch.randn(ns, 3, Ch, **dev), torch.randn(ns, H, P, N, **dev)
+    row, w, A = torch.randn(B, Ch + H, **dev), torch.randn(Ch, 4, **dev) * 0.4, -torch.rand(H, **dev) - 1
+    got = []
+    for s in (m, once):
+        c, hh, arr = conv.clone(), h.clone(), torch.zeros(ns, G, dtype=torch.int32, **dev)
+        y = ssd.ssd_mixer_step(c, hh, arr, row[:, :Ch], row[:, Ch:], w, A, dt_max=0.1,
+                               slots=torch.from_numpy(s.astype(np.int32)).cuda())
+        assert int(arr.abs().max()) == 0
+        got.append((y, c, hh))
+    for x, x2 in zip(*got):
+        assert torch.equal(x, x2)
+    off = torch.from_numpy((once < 0) | (once >= ns)).cuda()
+    assert float(got[0][0][off].abs().max()) == 0.0 and float(got[0][0][~off].abs().min(-1)[0].max()) > 0.0
