@@ -826,13 +826,11 @@ struct Arr {
   bool out;
 };
 
-// No output may share memory with another array of the call, except for a
-// pair of equal `may` entries (an update in place).
-int check_overlap(const Arr* v, int n, const void* may = nullptr) {
+// No output may share memory with another array of the call.
+int check_overlap(const Arr* v, int n) {
   for (int i = 0; i < n; ++i)
     for (int j = i + 1; j < n; ++j) {
       if (!v[i].out && !v[j].out) continue;
-      if (may && v[i].p == may && v[j].p == may && v[i].pitch == v[j].pitch) continue;
       const bool hit =
           v[i].rows == v[j].rows
               ? rows_overlap(v[i].p, v[i].pitch, v[i].bytes, v[j].p, v[j].pitch, v[j].bytes, v[i].rows)
@@ -871,13 +869,14 @@ int ssd_add_norm_fwd(const void* x, const float* scale, const void* residual, co
   SSD_TRY(check_ptr(residual_out, "residual_out", rs, false));
   SSD_TRY(check_ptr(out, "out", os, rows));
   const size_t m = M;
+  // in place, residual is residual_out, which shares with nothing else
   const Arr arrs[] = {{out, "out", d * os, d * os, m, true},
                       {residual_out, "residual_out", d * rs, d * rs, m, true},
-                      {residual, "residual", d * rs, d * rs, m, false},
+                      {residual == residual_out ? nullptr : residual, "residual", d * rs, d * rs, m, false},
                       {x, "x", d * xs, d * xs, m, false},
                       {w, "w", d * 4, d * 4, 1, false},
                       {scale, "scale", d * 4, d * 4, 1, false}};
-  SSD_TRY(check_overlap(arrs, 6, residual_out == residual ? residual : nullptr));
+  SSD_TRY(check_overlap(arrs, 6));
   if (!rows) return ok();
   ssd::AddNormArgs a{};
   a.x = x, a.scale = scale, a.residual = residual, a.w = w, a.eps = eps, a.r_out = residual_out;

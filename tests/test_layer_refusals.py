@@ -206,3 +206,26 @@ def test_mixer_step_refuses_a_batch_past_one_grid(B, H):
 def test_binding_passes_on_an_error_of_a_truth_value():
     with pytest.raises(RuntimeError, match="ambiguous"):
         ssd.ssd_conv1d_bwd(**conv_args(), want_dstate_in=z(2))
+
+
+IN_PLACE = dict(residual=ADD["residual"], ro=ADD["residual"])  # allowed: residual_out is residual
+
+
+@pytest.mark.parametrize("over,needle", [
+    (dict(out=ADD["residual"], od=0), "out and residual_out overlap"),   # r would be lost
+    (dict(x=ADD["residual"], xd=0), "residual_out and x overlap"),
+    (dict(w=ADD["residual"]), "residual_out and w overlap"),
+    (dict(w=ADD["residual"], M=1), "residual_out and w overlap"),
+    (dict(scale=ADD["residual"], M=1), "residual_out and scale overlap"),
+    (dict(out=ptr(128, (ADD["residual"].value - _base) // 4096), od=0), "out and residual_out overlap"),
+])
+def test_add_norm_fwd_in_place_shares_with_nothing_else(over, needle):
+    """The update in place excuses residual_out and residual, no other pair of
+    arrays at that address."""
+    refuse("ssd_add_norm_fwd", ADD, {**IN_PLACE, **over}, EINVAL, needle)
+
+
+def test_add_norm_fwd_in_place_is_accepted():
+    assert call("ssd_add_norm_fwd", ADD, dict(M=0, **IN_PLACE))[0] == ssd.SSD_OK
+    rc, msg = call("ssd_add_norm_fwd", ADD, dict(IN_PLACE, out=ADD["x"]))
+    assert rc == EINVAL and "out and x overlap" in msg  # no fault found with residual and residual_out
