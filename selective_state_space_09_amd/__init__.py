@@ -825,12 +825,15 @@ def _call(fn, t, stream, *args):
     current, so that what the call allocates belongs to the stream it runs on
     and the launch goes to t's device."""
     if stream is not None:
-        if stream.device != t.device:
+        if isinstance(t, torch.Tensor) and stream.device != t.device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {t.device}")
         with torch.cuda.stream(stream):
             r = fn(*args, stream.cuda_stream)
     else:
-        dev = t.get_device()
+        try:
+            dev = t.get_device()
+        except AttributeError:  # no tensor
+            dev = -1
         if dev < 0:
             r = fn(*args, 0)  # not a GPU tensor: refused by name
         elif dev == torch._C._cuda_getDevice():

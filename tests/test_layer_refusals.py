@@ -229,3 +229,24 @@ def test_add_norm_fwd_in_place_is_accepted():
     assert call("ssd_add_norm_fwd", ADD, dict(M=0, **IN_PLACE))[0] == ssd.SSD_OK
     rc, msg = call("ssd_add_norm_fwd", ADD, dict(IN_PLACE, out=ADD["x"]))
     assert rc == EINVAL and "out and x overlap" in msg  # no fault found with residual and residual_out
+
+
+def add_bwd_args():
+    return dict(dout=z(3, 8), r=z(3, 8), w=z(8))
+
+
+def gated_bwd_args():
+    return dict(dout=z(3, 8), y=z(3, 8), z=z(3, 8), w=z(8))
+
+
+@pytest.mark.parametrize("bad", [None, np.zeros((3, 8), np.float32), 1.0])
+@pytest.mark.parametrize("fn,args", [
+    ("ssd_add_norm_fwd", add_args), ("ssd_add_norm_bwd", add_bwd_args), ("ssd_gated_norm_fwd", gated_args),
+    ("ssd_gated_norm_bwd", gated_bwd_args), ("ssd_conv1d_bwd", conv_args), ("ssd_mixer_step", step_args)])
+def test_binding_names_what_is_no_tensor(fn, args, bad):
+    """Every required tensor, the one whose device the call goes to among them."""
+    for name in args():
+        if bad is None and name in ("residual", "scale", "arrivals"):
+            continue  # may be None
+        with pytest.raises(TypeError, match=f"^{name} must be a tensor"):
+            getattr(ssd, fn)(**{**args(), name: bad})
