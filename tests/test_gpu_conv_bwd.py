@@ -127,3 +127,70 @@ def test_conv_bwd_stream_graph_and_workspace():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(p, q) for p, q in zip(held, step())), k
+
+
+LONG = [
+    # Bsz, T, HP, GN, ld, col, type, state; run lengths as the plan has them at this writing
+    (9, 301, 2048, 64, 2184, 8, "f32", True),      # runs of 12, the last of one token
+    (7, 301, 4096, 128, 4352, 0, "bf16", False),   # 16
+    (4, 1203, 2048, 64, 2176, 0, "f32", True),     # 20, the last of three
+    (5, 1203, 2048, 64, 2184, 8, "bf16", True),    # 24, the last of three
+    (2, 2048, 4096, 128, 8512, 4096, "bf16", True),  # 28: the bf16 layer, in in_proj rows
+    (4, 2049, 2048, 64, 2176, 0, "bf16", True),    # 32, the last of one token
+    # more (sequence, run) units than a wave of the grid has one each
+    (8, 4096, 64, 8, 80, 0, "bf16", True),
+    (1, 20000, 32, 8, 56, 8, "f32", True),
+]
+
+
+@pytest.mark.parametrize("Bsz,T,HP,GN,ld,col,t,state", LONG)
+def test_conv_bwd_long_runs(Bsz, T, HP, GN, ld, col, t, state):
+    test_conv_bwd(Bsz, T, HP, GN, ld, col, t, 1, state, True)
+
+
+@pytest.mark.parametrize("T,t", [(5, "bf16"), (11, "f32")])
+def test_conv_bwd_more_units_than_waves(T, t):
+    """Sequences enough that every wave walks several: twice the largest
+    partial-sum table's rows times four waves, and some more."""
+    HP, GN = 64, 8
+    parts = ssd.ssd_conv1d_bwd_workspace_size(65535, T, HP, GN) // (20 * (HP + 2 * GN))
+    test_conv_bwd(4 * parts * 2 + 77, T, HP, GN, 80, 0, t, 1, True, True)
+
+
+def test_conv_bwd_past_32_bit_offsets():
+    """One sequence of 2^31 + elements with gradients at its two ends: rows,
+    sums and the carried state's gradient against the oracle on the ends, and
+    no gradient between them."""
+    HP, GN, T, E, Z = 2032, 8, (1 << 20) + 40, 48, 8  # ends of 48 tokens, the inner 8 without gradient
+    Ch = HP + 2 * GN
+    rng = np.random.default_rng(10)
+    w, bias, st, dso = normal(rng, (Ch, 4), mul=0.5), normal(rng, Ch, mul=0.5), normal(rng, (1, 3, Ch)), normal(rng, (1, 3, Ch))
+    ends = [dict(x=normal(rng, (1, E, Ch), "bf16"), dx=normal(rng, (1, E, HP), "bf16"), dB=normal(rng, (1, E, GN)),
+                 dC=normal(rng, (1, E, GN))) for _ in range(2)]
+    for e, quiet in zip(ends, (slice(E - Z, E), slice(0, Z))):
+        for k in ("dx", "dB", "dC"):
+            e[k][:, quiet] = 0
+    make = lambda n, t, fill: torch.full((1, T, n), fill, dtype=t, device="cuda")  # noqa: E731
+    d = dict(x=make(Ch, torch.bfloat16, 1.0), dx=make(HP, torch.bfloat16, 0.0), dB=make(GN, torch.float32, 0.0),
+             dC=make(GN, torch.float32, 0.0))
+    for k, v in d.items():
+        v[:, :E], v[:, -E:] = _gpu.to_dev(ends[0][k]), _gpu.to_dev(ends[1][k])
+    up = _gpu.to_dev
+    got = ssd.ssd_conv1d_bwd(d["x"], up(w), d["dx"], d["dB"], d["dC"], bias=up(bias), state_in=up(st), dstate_out=up(dso))
+    ones = np.ones((1, 3, Ch), np.float32)  # the inputs before the last tokens
+    sums = {}
+    for e, s, o, rows in ((ends[0], st, None, slice(0, E)), (ends[1], ones, dso, slice(T - E, T))):
+        dout = np.concatenate([wide(e["dx"]), e["dB"], e["dC"]], 2).astype(np.float64)
+        ref = layer.conv1d_bwd(e["x"], w, dout, bias, s, o, 1)
+        seq = np.concatenate([np.abs(wide(s)), np.abs(wide(e["x"]))], 1)
+        v = 1.0 + np.abs(wide(bias)) + sum(np.abs(wide(w))[:, j] * seq[:, j:j + E] for j in range(4))
+        mag = layer.conv1d_bwd(seq[:, 3:], np.abs(w), np.abs(dout) * v, None, seq[:, :3], None if o is None else np.abs(o), 0)
+        within(got["dxbc"][:, rows], ref["dxbc"], "bf16", C, mag["dxbc"], "dxbc")
+        if o is None:
+            within(got["dstate_in"], ref["dstate_in"], "f32", C, mag["dstate_in"], "dstate_in")
+        for k in ("dw", "dbias"):
+            a, b = sums.get(k, (0.0, 0.0))
+            sums[k] = a + ref[k], b + mag[k]
+    assert float(got["dxbc"][:, E:T - E].abs().max()) == 0.0
+    for k, (ref, mag) in sums.items():  # the terms between the ends are zeros, which add no rounding
+        within(got[k], ref, "f32", C + 2 * E / 8 + 80, mag, k)
