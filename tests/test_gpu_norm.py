@@ -283,3 +283,97 @@ def test_norms_on_another_stream_and_in_a_graph():
         torch.cuda.synchronize()
         for a, b in zip(held, step()):
             assert torch.equal(a, b), k
+
+
+def walked(parts, rows):
+    """A number of rows at which every team of a backward pass walks `rows`
+    rows and some one more.  parts(M): the rows of its partial-sum table, one
+    per workgroup."""
+    most = parts(1 << 20)
+    teams = next(m for m in range(1, 1 << 10) if parts(m + 1) == 2)  # one row a team fills the first workgroup
+    return most * teams * rows + most * teams // 3 + 1
+
+
+WALKED_ADD = [
+    # D, x, residual's, out's type, residual?, scale?
+    (64, "bf16", "f32", "bf16", True, True),      # 16-lane teams
+    (512, "f32", "f32", "bf16", True, True),      # a wave
+    (1000, "bf16", "bf16", "f32", False, True),   # a wave, two vectors a lane
+    (1027, "f32", "f32", "f32", True, True),      # from here on a workgroup per row: a barrier in the walk
+    (2048, "bf16", "f32", "bf16", True, True),
+    (2049, "bf16", "f32", "f32", True, False),
+    (4100, "f32", "bf16", "bf16", True, True),
+    (8200, "f32", "f32", "f32", True, True),      # the widest, two vectors a lane
+    (16383, "bf16", "f32", "bf16", True, True),
+]
+
+
+@pytest.mark.parametrize("D,x,res,out,with_res,with_scale", WALKED_ADD)
+def test_add_norm_bwd_walks_rows(D, x, res, out, with_res, with_scale):
+    M = walked(lambda m: ssd.ssd_add_norm_bwd_workspace_size(m, D) // (8 * D), 3)
+    test_add_norm_bwd(M, D, x, res, out, with_res, with_scale)
+
+
+WALKED_GATED = [
+    # D, groups, ld, col, y, z, out, before
+    (128, 1, 136, 4, "bf16", "f32", "bf16", False),
+    (500, 1, 1003, 3, "bf16", "bf16", "f32", True),
+    (1024, 1, 1024, 0, "f32", "bf16", "bf16", False),
+    (2048, 1, 2056, 8, "bf16", "bf16", "bf16", False),
+    (2048, 1, 2048, 0, "f32", "f32", "f32", True),
+    (4096, 1, 4100, 1, "f32", "bf16", "f32", False),
+    (4096, 8, 8512, 0, "bf16", "bf16", "bf16", False),
+    (6000, 2, 6001, 1, "bf16", "f32", "bf16", True),
+    (8192, 1, 8200, 0, "f32", "bf16", "f32", False),
+    (16384, 1, 16384, 0, "f32", "f32", "bf16", False),
+]
+
+
+@pytest.mark.parametrize("D,groups,ld,col,y,z,out,before", WALKED_GATED)
+def test_gated_norm_bwd_walks_rows(D, groups, ld, col, y, z, out, before):
+    M = walked(lambda m: ssd.ssd_gated_norm_bwd_workspace_size(m, D, groups) // (4 * D), 3)
+    test_gated_norm_bwd(M, D, groups, ld, col, y, z, out, before)
+
+
+@pytest.mark.parametrize("M,D", [(40000, 300), (4096 * 3 + 5, 1027), (4096 * 3 + 5, 2100)])
+def test_norms_forward_walk_rows(M, D):
+    """More rows than the forward has teams for (4096 workgroups)."""
+    test_add_norm_fwd(M, D, "bf16", "f32", "bf16", True, True)
+    test_gated_norm_fwd(M, D, 1, D + 3, 1, "bf16", "bf16", "bf16", False)
+
+
+def test_gradients_past_32_bit_offsets():
+    """Backward passes over 2^31 + elements: the last rows equal a call on them
+    alone, the rows between have no gradient, and the sums over rows are those
+    of the first and last rows."""
+    D, M, E = 2048, (1 << 20) + 8, 8
+    rng = np.random.default_rng(9)
+    ends = normal(rng, (2 * E, D), "bf16")
+    dends, w = normal(rng, (2 * E, D), "bf16"), normal(rng, D, mul=0.2, add=1.0)
+    r = torch.ones(M, D, dtype=torch.bfloat16, device="cuda")
+    dout = torch.zeros(M, D, dtype=torch.bfloat16, device="cuda")
+    for t, v in ((r, _gpu.to_dev(ends)), (dout, _gpu.to_dev(dends))):
+        t[:E], t[-E:] = v[:E], v[E:]
+    wd = _gpu.to_dev(w)
+    rstd = 1 / np.sqrt((wide(ends) ** 2).mean(-1, keepdims=True) + EPS)
+    n, dn = np.abs(wide(ends)) * rstd, np.abs(wide(dends) * wide(w))
+    mag = (np.abs(wide(dends)) * n).sum(0)
+    g = ssd.ssd_add_norm_bwd(dout, r, wd, x=r)
+    tail = ssd.ssd_add_norm_bwd(dout[-E:], r[-E:], wd, x=r[-E:])
+    for k in ("dresidual", "dx"):
+        assert torch.equal(g[k][-E:], tail[k])
+        assert float(g[k][E:-E].abs().max()) == 0.0
+    ref = layer.add_norm_bwd(dends, ends, w, x=ends, eps=EPS)
+    within(g["dw"], ref["dw"], "f32", rows_c(2 * E), mag, "dw")
+    rmag = rstd * (dn + n * (dn * n).mean(-1, keepdims=True))
+    within(g["dscale"], ref["dscale"], "f32", rows_c(2 * E), (rmag * np.abs(wide(ends))).sum(0), "dscale")
+    del g
+    h = ssd.ssd_gated_norm_bwd(dout, r, r, wd)
+    tail = ssd.ssd_gated_norm_bwd(dout[-E:], r[-E:], r[-E:], wd)
+    for k in ("dy", "dz"):
+        assert torch.equal(h[k][-E:], tail[k])
+        assert float(h[k][E:-E].abs().max()) == 0.0
+    ref = layer.gated_norm_bwd(dends, ends, ends, w, 1, EPS)
+    u = np.abs(wide(ends) * layer.silu(wide(ends)))
+    n = u / np.sqrt((u * u).mean(-1, keepdims=True) + EPS)
+    within(h["dw"], ref["dw"], "f32", rows_c(2 * E), (np.abs(wide(dends)) * n).sum(0), "gated dw")
