@@ -575,9 +575,10 @@ int ssd_mimo_fwd(const void *y, int y_dtype, const void *W, void *z,
  *   out          (M, D)  out_dtype, rounded once
  * M >= 0 rows of D channels, 1 <= D <= 16384, any alignment of the element
  * size.  eps >= 0 (0 with a row of zeros gives NaN, as the formula does).  Sums
- * are float32: |r| stays below about 1e18 (its squares do not overflow).  Apart
- * from residual_out being `residual`, outputs must not overlap each other or
- * any input (such a call is rejected).  Errors: SSD_EINVAL, SSD_EUNSUPPORTED
+ * are float32: a row's largest |r| may be up to 1e18 and, with eps 0, has to be
+ * 1e-18 or more (in the gated norm the same holds of what it normalises).
+ * Apart from residual_out being `residual`, outputs must not overlap each other
+ * or any input (such a call is rejected).  Errors: SSD_EINVAL, SSD_EUNSUPPORTED
  * (dtype, D), SSD_EHIP.
  */
 int ssd_add_norm_fwd(const void *x, const float *scale, const void *residual,

@@ -88,6 +88,12 @@ __device__ __forceinline__ void own_sum(float& acc, int drop, F f) {
   }
 }
 
+// A lane's sum of squares is scaled by a power of two before the team's sum and
+// back in the mean.  No bit of an ordinary row changes, and 16384 squares of
+// 1e18 stay inside float32 (2.6e38); unscaled they pass it, rsqrt gives 0 and
+// the row is lost.  The other end moves by 2^3: squares of 1e-18 stay whole.
+constexpr float kDown = 1.0f / 64.0f, kUp = 64.0f;
+
 // Threads of a workgroup: `several` shared by teams of up to a wave, which
 // need no barrier in their row loops; a wider team has a workgroup of its own.
 template <int TPR>
@@ -103,7 +109,7 @@ __global__ __launch_bounds__(team_block<TPR>(kFwdThreads)) void ssd_add_norm_ker
   constexpr int BT = team_block<TPR>(kFwdThreads), TEAMS = BT / TPR;
   __shared__ float red[TPR > kWave ? 32 : 1];
   const int lane = threadIdx.x % TPR;
-  const float inv = 1.0f / static_cast<float>(D);
+  const float inv = kUp / static_cast<float>(D);
   Place pl[K];
 #pragma unroll
   for (int k = 0; k < K; ++k) pl[k] = place_of<SHORT>(lane + k * TPR, D);
@@ -145,6 +151,7 @@ __global__ __launch_bounds__(team_block<TPR>(kFwdThreads)) void ssd_add_norm_ker
     float ss[1] = {0.0f};
 #pragma unroll
     for (int k = 0; k < K; ++k) own_sum(ss[0], pl[k].drop, [&](int i) { return r[k][i] * r[k][i]; });
+    ss[0] *= kDown;
     team_sum<TPR, 1>(ss, red, parity);
     parity ^= 1;
     const float rstd = rsqrtf(ss[0] * inv + eps);
@@ -234,9 +241,10 @@ __global__ __launch_bounds__(team_block<TPR>(kBwdThreads)) void ssd_add_norm_bwd
       own_sum(s[0], pl[k].drop, [&](int i) { return rv[k][i] * rv[k][i]; });
       own_sum(s[1], pl[k].drop, [&](int i) { return dv[k][i] * wv[i] * rv[k][i]; });
     }
+    s[0] *= kDown;
     team_sum<TPR, 2>(s, red, parity);
     parity ^= 1;
-    const float rstd = rsqrtf(s[0] * inv + eps);
+    const float rstd = rsqrtf(s[0] * (kUp * inv) + eps);
     const float m = s[1] * rstd * inv;  // mean(dn o n)
 #pragma unroll
     for (int k = 0; k < K; ++k) {
@@ -279,7 +287,7 @@ __global__ __launch_bounds__(team_block<TPR>(kFwdThreads)) void ssd_gated_norm_k
   constexpr int BT = team_block<TPR>(kFwdThreads), TEAMS = BT / TPR;
   __shared__ float red[TPR > kWave ? 32 : 1];
   const int lane = threadIdx.x % TPR;
-  const float inv = 1.0f / static_cast<float>(L);
+  const float inv = kUp / static_cast<float>(L);
   const size_t c0 = static_cast<size_t>(blockIdx.y) * L;
   Place pl[K];
 #pragma unroll
@@ -310,6 +318,7 @@ __global__ __launch_bounds__(team_block<TPR>(kFwdThreads)) void ssd_gated_norm_k
       }
       own_sum(ss[0], pl[k].drop, [&](int i) { return u[k][i] * u[k][i]; });
     }
+    ss[0] *= kDown;
     team_sum<TPR, 1>(ss, red, parity);
     parity ^= 1;
     const float rstd = rsqrtf(ss[0] * inv + eps);
@@ -365,9 +374,10 @@ __global__ __launch_bounds__(team_block<TPR>(kBwdThreads)) void ssd_gated_norm_b
       own_sum(s[0], pl[k].drop, [&](int i) { return u[i] * u[i]; });
       own_sum(s[1], pl[k].drop, [&](int i) { return dn[i] * wv[i] * u[i]; });
     }
+    s[0] *= kDown;
     team_sum<TPR, 2>(s, red, parity);
     parity ^= 1;
-    const float rstd = rsqrtf(s[0] * inv + eps);
+    const float rstd = rsqrtf(s[0] * (kUp * inv) + eps);
     const float m = s[1] * rstd * inv;
 #pragma unroll
     for (int k = 0; k < K; ++k) {

@@ -342,6 +342,46 @@ def test_norms_forward_walk_rows(M, D):
     test_gated_norm_fwd(M, D, 1, D + 3, 1, "bf16", "bf16", "bf16", False)
 
 
+@pytest.mark.parametrize("D", [1, 7, 300, 1027, 2048, 8200, 16384])
+@pytest.mark.parametrize("size,eps", [(1e18, 1e-5), (1e-18, 0.0)])
+def test_norms_over_the_range_of_values(D, size, eps):
+    """Rows of values up to 1e18, whose squares alone add up past float32, and
+    down to 1e-18 with eps 0: within the bars of ordinary rows."""
+    print(f"norms over the range D={D} size={size} eps={eps}", flush=True)
+    rng = np.random.default_rng(D)
+    M = 5
+    r = (rng.uniform(0.5, 1.0, (M, D)) * rng.choice([-1.0, 1.0], (M, D)) * size).astype(np.float32)
+    w, dout = normal(rng, D, mul=0.2, add=1.0), normal(rng, (M, D))
+    up = _gpu.to_dev
+    out, kept = ssd.ssd_add_norm_fwd(up(r), up(w), eps=eps)
+    ref, _ = layer.add_norm(r, w, eps=eps)
+    assert torch.equal(kept, up(r))
+    within(out, ref, "f32", C_FWD, 2 * np.abs(ref), "out")
+    g = ssd.ssd_add_norm_bwd(up(dout), up(r), up(w), eps=eps)
+    gref = layer.add_norm_bwd(dout, r, w, eps=eps)
+    rstd = 1 / np.sqrt((wide(r) ** 2).mean(-1, keepdims=True) + eps)
+    n, dn = np.abs(wide(r) * rstd), np.abs(wide(dout) * wide(w))
+    within(g["dx"], gref["dx"], "f32", C_BWD, rstd * (dn + n * (dn * n).mean(-1, keepdims=True)), "dx")
+    within(g["dw"], gref["dw"], "f32", rows_c(M), (np.abs(wide(dout)) * n).sum(0), "dw")
+    # the gated norm's u = y silu(z): 1e9 each way, or a small y
+    big = size > 1
+    y = (r / np.float32(1e9) if big else r).astype(np.float32)
+    z = (rng.uniform(1.0, 4.0, (M, D)) * (2.5e8 if big else 1.0)).astype(np.float32)
+    ref = layer.gated_norm(y, z, w, 1, eps)
+    within(ssd.ssd_gated_norm_fwd(up(y), up(z), up(w), eps=eps), ref, "f32", C_GATE, np.abs(ref), "gated")
+    h = ssd.ssd_gated_norm_bwd(up(dout), up(y), up(z), up(w), eps=eps)
+    href = layer.gated_norm_bwd(dout, y, z, w, 1, eps)
+    Y, Z = np.abs(wide(y)), np.abs(wide(z))
+    sig = layer.sigmoid(Z)
+    u = Y * Z * sig
+    rstd = 1 / np.sqrt((u * u).mean(-1, keepdims=True) + eps)
+    n = u * rstd
+    du = rstd * (dn + n * (dn * n).mean(-1, keepdims=True))
+    within(h["dy"], href["dy"], "f32", C_BWD, du * Z * sig, "dy")
+    within(h["dz"], href["dz"], "f32", C_BWD, du * Y * sig * (1 + Z * (1 - sig)), "dz")
+    within(h["dw"], href["dw"], "f32", rows_c(M), (np.abs(wide(dout)) * n).sum(0), "gated dw")
+
+
 def test_gradients_past_32_bit_offsets():
     """Backward passes over 2^31 + elements: the last rows equal a call on them
     alone, the rows between have no gradient, and the sums over rows are those
