@@ -11,7 +11,7 @@
 // forward.
 //
 // The operation streams (x and dout in, dx out).  A lane owns V channels and
-// walks a run of kRun tokens with the windows of inputs and gradients and the
+// walks a run of 8 to 32 tokens with the windows of inputs and gradients and the
 // channels' five sums in registers, so a row is read once per run (plus halo
 // rows that the cache serves).  To write din_p it needs g up to p + 3: it
 // starts with g_{t0..t0+2} and then, for each p, makes g_{p+3} and din_p.  The
@@ -57,16 +57,14 @@ constexpr uint32_t kOut = 0x60000000u;
 template <typename T, int V>
 struct Raw {
   static constexpr int BYTES = sizeof(T) * V, WORDS = BYTES / 4;
+  static_assert(BYTES == 4 || BYTES == 8, "one or two words");
   uint32_t w[WORDS];
   __device__ __forceinline__ void load(buf_t b, uint32_t off) {
     if constexpr (BYTES == 4) {
       w[0] = __builtin_amdgcn_raw_buffer_load_b32(b, off, 0, 0);
-    } else if constexpr (BYTES == 8) {
+    } else {
       const uint2 q = buf_load8(b, off);
       w[0] = q.x, w[1] = q.y;
-    } else {
-      const uint4 q = buf_load16(b, off);
-      w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
     }
   }
   __device__ __forceinline__ float at(int v) const {
@@ -80,10 +78,8 @@ struct Raw {
       w[i] = sizeof(T) == 4 ? __float_as_uint(f[i]) : pack_bf16x2(f[2 * i], f[2 * i + 1]);
     if constexpr (BYTES == 4)
       __builtin_amdgcn_raw_buffer_store_b32(w[0], b, off, 0, 0);
-    else if constexpr (BYTES == 8)
-      buf_store8(b, off, make_uint2(w[0], w[1]));
     else
-      buf_store16(b, off, make_uint4(w[0], w[1], w[2], w[3]));
+      buf_store8(b, off, make_uint2(w[0], w[1]));
   }
 };
 
