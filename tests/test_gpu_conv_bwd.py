@@ -6,8 +6,9 @@ the sigmoid of the hardware exponential and reciprocal at |v| < 12 (1.5 |v| + 6
 C = 40.  Since v's error moves the derivative by at most |v error| (|SiLU''| <=
 1/2), v's own magnitude enters through it: the bars' magnitude takes
 |dout| (1 + sum |w in| + |bias|).  A sum over n tokens adds at most n / 8 + 80
-terms in sequence (32 or more tokens in a run, 4 runs, then the parts in four
-interleaved chains)."""
+terms in sequence: a wave's tokens (one run of 8 to 32 and its first three; past
+1024 runs in a call n / 1024 and at most a run more), 4 waves, then at most 256
+parts in 16 chains and the chains."""
 import numpy as np
 import pytest
 import torch
@@ -27,13 +28,13 @@ CASES = [
     (3, 2, 16, 0, 16, 0, "f32", 1, True, True),       # no B and C, shorter than the kernel
     (1, 3, 16, 8, 40, 8, "bf16", 1, True, True),
     (2, 0, 16, 8, 32, 0, "f32", 1, True, True),       # no tokens: the state's gradient passes through
-    (2, 31, 64, 16, 104, 8, "f32", 1, False, True),   # one token short of a run
-    (1, 33, 64, 16, 96, 0, "bf16", 1, False, False),  # one past it
+    (2, 31, 64, 16, 104, 8, "f32", 1, False, True),   # one token short of four runs of 8
+    (1, 33, 64, 16, 96, 0, "bf16", 1, False, False),  # one past them
     (2, 200, 96, 16, 136, 8, "bf16", 1, False, True),
     (1, 70, 512, 64, 704, 64, "bf16", 1, True, True),
     (2, 129, 512, 64, 640, 0, "f32", 1, True, True),
     (1, 257, 64, 32, 128, 0, "f32", 0, True, True),
-    (300, 5, 64, 8, 80, 0, "bf16", 1, True, True),    # more sequences than parts hold runs
+    (300, 5, 64, 8, 80, 0, "bf16", 1, True, True),    # many sequences shorter than a run: 75 parts of 4
 ]
 
 

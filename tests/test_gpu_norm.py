@@ -44,7 +44,7 @@ ADD = [
     (3, 8191, "bf16", "f32", "bf16", True, True),
     (2, 16384, "bf16", "bf16", "bf16", True, True),     # the longest row
     (2, 16383, "f32", "f32", "f32", True, True),
-    (5000, 64, "bf16", "f32", "bf16", True, True),      # more rows than teams: partial sums over 313 parts
+    (5000, 64, "bf16", "f32", "bf16", True, True),      # many short rows, one to a team: partial sums over 157 parts
 ]
 
 
