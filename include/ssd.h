@@ -660,9 +660,9 @@ int ssd_gated_norm_bwd(const void *dout, const void *y, const void *z,
  *              tokens, written even when bias is NULL
  *   dstate_in  (Bsz, 3, Ch) float32, or NULL (not written)
  *   workspace  ssd_conv1d_bwd_workspace_size(...) bytes, 256-byte aligned
- * HP, GN, ld and lddx multiples of 8 (bf16) or 4 (fp32), pointers 16-byte
- * aligned, T <= 2^30, Ch <= 2^24.  T = 0: dstate_in is dstate_out, the sums
- * are zero.  Sums in a fixed order (no atomics).  Outputs must not overlap
+ * HP, GN, ld and lddx multiples of 8 (bf16) or 4 (fp32), ld and lddx below
+ * 2^31, pointers 16-byte aligned, Bsz <= 65535, T <= 2^30, Ch <= 2^24.  T = 0:
+ * dstate_in is dstate_out, the sums are zero.  Sums in a fixed order (no atomics).  Outputs must not overlap
  * anything (such a call is rejected).
  */
 size_t ssd_conv1d_bwd_workspace_size(int Bsz, int T, int HP, int GN);

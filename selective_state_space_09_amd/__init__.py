@@ -924,7 +924,7 @@ def ssd_mixer_step(conv_state, h, arrivals, xbc, dt, w, A, bias=None, D=None, dt
     made, then the library's; None allowed when H == G).  slots (Bsz) int32 on
     the GPU maps rows to slots (None: row b has slot b); a row whose slot is
     outside the pool, or taken by an earlier row, is padding: its y is zero.
-    xbc (Bsz,Ch) and dt (Bsz,H) float32 or bfloat16, contiguous or column slices
-    of the in_proj rows.  Returns y (Bsz,H,P) in y_dtype."""
+    xbc (Bsz,Ch) and dt (Bsz,H) both float32 or both bfloat16, contiguous or
+    column slices of the in_proj rows.  Returns y (Bsz,H,P) in y_dtype."""
     return _call(native().mixer_step, h, stream, conv_state, h, arrivals, xbc, dt, w, A, bias, D,
                  dt_bias, dt_min, dt_max, slots, act, y, _code(y_dtype, "y"))

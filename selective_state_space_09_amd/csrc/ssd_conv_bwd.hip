@@ -29,9 +29,12 @@
 // partial-sum table that a second kernel adds up in a fixed order.
 //
 // What bounds it: the bytes (2 x 2048 tokens of 4352 bf16 channels: 109 MB, 21.7
-// us as one elementwise library kernel) and, close behind, the VALU: 30
-// instructions per element, two of them quarter-rate, 14.5 us.  24 us for this
-// kernel and 4 for the sums: 28.1 us, 3.9 TB/s.
+// us as one elementwise library kernel) and, close behind, the instructions: 30
+// of the VALU per element, two of them quarter-rate, 14.8 us, and three scalar
+// ones to every four of them (the descriptors; with SiLU 13 or 14 scalar registers
+// are spilled to vector lanes).  28.3 us a call, 3.9 TB/s; in a trace 26.9 us (25.4
+// at least) for this kernel and 4.0 for the sums.  Few channels leave lanes idle:
+// 8 x 4096 tokens of 80 bf16 channels 21.7 us, 0.8 TB/s.
 
 #include "ssd_chunk_common.h"
 #include "ssd_internal.h"
@@ -313,7 +316,10 @@ __global__ __launch_bounds__(kThreads) void ssd_conv1d_bwd_kernel(
 // halo: three more gradients, six more rows), and the CU with the most
 // workgroups ends last, so of the runs that give kMinWaves waves (four per SIMD)
 // the one with the least ceil(workgroups / CUs) (n + 5); without enough waves
-// the shortest.  Measured (both kernels): 2 x 2048 tokens of 4352 bf16 channels,
+// the shortest.  The ranking counts a workgroup for every four runs, also past the
+// kMaxParts per channel block that are launched (waves then walk several runs), so
+// few channels with many tokens are ranked by a grid that is not quite theirs.
+// Measured (both kernels): 2 x 2048 tokens of 4352 bf16 channels,
 // 1258 workgroups of 28-token runs 28.1 us, 1088 of 32 30.0 (five on some CUs,
 // 4.25 on average), 1768 of 20 29.1; 3 x 509 tokens of 1024 + 2 x 1024 float32
 // channels, runs of 8 (4608 waves) 16.4, of 12 17.0, of 32 18.5.

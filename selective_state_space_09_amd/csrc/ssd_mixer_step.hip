@@ -35,9 +35,15 @@
 // H = P = 64, N = 128 2976 us, without a slot map 2797, with one load at a time
 // 3631; 16384 rows of H = 8, P = 32, N = 16 767, 492 and 2521.
 //
-// Measured at 256 rows of H = P = 64, N = 128, one group (1.11 GB): 189 us, 5.9
-// TB/s; ssd_conv1d_step and ssd_step_decode on the same states in slot order
-// take 6.0 + 178 us.
+// Measured at 256 rows of H = P = 64, N = 128, one group (1.11 GB): 190 us, 5.8
+// TB/s.  ssd_conv1d_step and ssd_step_decode on the same states, their float32
+// inputs ready and row b on slot b, take 6.1 + 180 us there, 3.4 + 45.0 at 64 rows
+// (this kernel 53.5), 2.8 + 24.8 at 32 (30.3), 2.7 + 13.4 at 16 (16.7), 2.6 + 7.7
+// at 8 (10.2) and 2.5 + 4.8 at one (6.7).  From 16 rows on the one launch takes
+// more than the two together, most at 32 rows: 1024 workgroups of nine waves and
+// 72 registers, of which 768 are resident.  What it gives for that are slots and
+// padding in a pool, and bf16 in_proj rows read in place, which the two kernels'
+// caller first has to gather and widen.
 
 #include "ssd_chunk_common.h"
 #include "ssd_internal.h"

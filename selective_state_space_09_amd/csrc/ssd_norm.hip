@@ -24,14 +24,16 @@
 // join them in LDS and write one row of a partial-sum table, which a second
 // kernel adds up in a fixed order (no atomics).
 //
-// Measured (a 1 GiB copy reaches 4.98 TB/s, a 64 MB one in the cache 6.8):
-//   residual norm, 16384 x 2048, bf16 x and out, float32 r:  78.9 us, 5.1 TB/s
-//     backward, 4096 x 2048, with dscale:  32.7 us in all, 28 + 4.5 us for the
-//     sums (4.6 TB/s; two library adds over the same bytes take 31.1 us)
-//     backward, 1237 x 1027, float32:  13.6 us, 10 + 4 (in the cache)
-//     one row of 2048:  2.4 us (a launch)
-//   gated norm, 4096 x 4096 bf16, z in rows of 8512:  17.4 us, 5.8 TB/s
-//     backward in 8 groups:  34.3 us in all (4.9 TB/s)
+// Measured in a captured graph, and for a backward its two kernels in a trace (a
+// 1 GiB copy reaches 4.98 TB/s, a 64 MB one in the cache 6.8):
+//   residual norm, 16384 x 2048, bf16 x and out, float32 r:  79.0 us, 5.1 TB/s
+//     backward, 4096 x 2048, with dscale:  32.8 us (4.6 TB/s), 29.9 + 4.1 for
+//     the sums; two library adds over the same bytes take 31.1 us
+//     backward, 1237 x 1027, float32:  13.8 us, 10.6 + 4.1 (in the cache; 1027
+//     channels are 129 vectors for 256 lanes, and 512 workgroups walk 2 or 3 rows)
+//     one row of 2048:  2.5 us (a launch)
+//   gated norm, 4096 x 4096 bf16, z in rows of 8512:  17.6 us, 5.7 TB/s
+//     backward in 8 groups:  34.4 us (4.9 TB/s), 31.8 + 4.0
 //     256 x 4096, float32 y:  3.4 us
 // Set aside: the next row's loads issued before a row is processed (residual
 // backward 37.5 -> 36.9 us, gated 39.9 -> 42.5, before the weights stayed in
@@ -444,17 +446,26 @@ __global__ __launch_bounds__(kSumWaves* kWave) void ssd_sum_parts_kernel(
 struct Shape {
   int tpr, k;
 };
-// Lanes of a team and vectors per lane for a row segment of L elements.
-// Forward: one vector per lane up to 8192 elements.  The few instructions per
-// wave set the time of a small batch (one row of 2048: 256 lanes 2.7 us, 64
-// lanes of four vectors 3.4), and large batches stream either way (4096 x 2048:
-// 17.1 and 16.9 us; 512 x 16384: 19.7 and, with 512 lanes of four, 17.5).
+// Lanes of a team and vectors per lane for a row segment of L elements, in both
+// directions.
+// Forward: one vector per lane, but for the longest rows and for 513 to 1024
+// elements, whose backward is the faster with two (below).  The few instructions
+// per wave set the time of a small batch (one row of 2048: 256 lanes 2.7 us, 64
+// lanes of four vectors 3.4; one row of 1024 with two 2.6), and large batches
+// stream either way (4096 x 2048: 17.1 and 16.9 us, 8192 x 1024 with two 16.9;
+// 512 x 16384: 19.7 and, with 512 lanes of four, 17.5).
 // Backward: each lane also holds the column sums of its vectors.  Measured for
 // the residual norm (bf16 x and dout, float32 r and dres, 2^23 elements) and,
 // after the slash, the gated one (bf16, 2^24), floors 30.3 / 33.7 us: L = 512
 // 32.6 / 33.4 us; 1024 with 64 lanes of two 33.1 / 34.0, 128 of one 35.0 / 42.1;
 // 2048 32.2 / 36.5; 4096 34.7 / 36.6; 8192 with 1024 of one 37.3 / 41.0, 512 of
 // two 44.5 / 44.1; 16384 with 1024 of two 44.1, 512 of four 45.8.
+// Other types cross register limits, but not the time: the gated backward of 2049
+// to 4096 channels with float32 y and bf16 z takes 130 registers, so one workgroup
+// a CU instead of two (4096 x 4096: 1.14 of its floor; all bf16, 123 registers,
+// 1.17); of 4097 to 8192 channels it spills 1 to 4 with a float32 among its types
+// (1.01 to 1.05; all bf16, none, 1.22); the residual backward of 8193 to 16384
+// channels spills 2 to 17 (512 x 16384: 1.41 to 1.46; all bf16, none, 1.68).
 Shape shape_of(int L) {
   if (L <= 128) return {16, 1};
   if (L <= 512) return {64, 1};
